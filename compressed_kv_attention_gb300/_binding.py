@@ -32,10 +32,16 @@ class CkvCacheStruct(ctypes.Structure):
                 ("v_signs", ctypes.c_void_p), ("v_signs2", ctypes.c_void_p)]
 
 
+class CkvScoreStruct(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+                ("prefix_len", ctypes.c_void_p), ("doc_start", ctypes.c_void_p)]
+
+
 _lib = None
 
 _c_int, _c_i64, _c_size, _c_f, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float, ctypes.c_void_p
 _cache_p = ctypes.POINTER(CkvCacheStruct)
+_score_p = ctypes.POINTER(CkvScoreStruct)
 
 SIGNATURES = {
     "ckv_version": (_c_int, []),
@@ -82,6 +88,13 @@ SIGNATURES = {
     "ckv_attn_prefill_shared_workspace": (_c_size, [_cache_p, _c_int, _c_i64, _c_int, _c_int]),
     "ckv_attn_prefill_shared": (_c_int, [_cache_p, _c_i64, _vp, _vp, _c_i64, _vp, _c_int, _vp, _vp, _vp, _c_int,
                                          _c_int, _c_f, _vp, _vp, _vp, _c_size, _vp]),
+    "ckv_attn_scored_workspace": (_c_size, [_cache_p, _c_i64, _c_int, _c_int, _c_int]),
+    "ckv_attn_scored": (_c_int, [_cache_p, _vp, _c_i64, _vp, _c_int, _c_int, _c_int, _vp, _c_f, _score_p, _c_int, _vp,
+                                 _c_int, _vp, _vp, _c_size, _vp]),
+    "ckv_attn_tree_workspace": (_c_size, [_cache_p, _c_i64, _c_int, _c_int, _c_int]),
+    "ckv_attn_tree": (_c_int, [_cache_p, _vp, _c_i64, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_f, _score_p, _c_int,
+                               _vp, _c_int, _vp, _vp, _c_size, _vp]),
+    "ckv_tree_accept": (_c_int, [_cache_p, _vp, _c_int, _vp, _vp, _c_int, _vp, _vp, _vp, _vp]),
     "ckv_read_device_flag": (_c_int, [_vp, ctypes.POINTER(_c_int), _vp]),
     "ckv_set_concurrent_kernels": (None, [_c_int]),
     "ckv_read_noalloc_flag": (_c_int, [ctypes.POINTER(_c_int), _vp]),
@@ -375,6 +388,92 @@ def attn_prefill_shared(prefix: PackedCache, n_prefix: int, k_tail, v_tail, tail
                                           _ptr(tail_len), n_agents, _ptr(q), _ptr(k_new), _ptr(v_new), n_new,
                                           n_q_heads, scale, _ptr(out), _ptr(lse), _ptr(workspace),
                                           workspace.numel(), _stream(stream)))
+
+
+def _dtype_code(t, what: str) -> int:
+    import torch
+    codes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+    if t.dtype not in codes:
+        raise TypeError(f"{what} must be float32, float16 or bfloat16, got {t.dtype}")
+    return codes[t.dtype]
+
+
+def _expect(t, what: str, shape, *dtypes):
+    """Optional device tensors of the scored calls: exact shape, a listed type, contiguous."""
+    if t is None:
+        return
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous tensor of shape {tuple(shape)} and type "
+                         f"{' or '.join(map(str, dtypes))}, got {tuple(t.shape)}, {t.dtype}")
+
+
+def _scored_tensors(cache, seq_len, q, out, lse, q_len, slopes):
+    import torch
+    B, n_q, n_q_heads, D = q.shape
+    if (B, D) != (cache.batch, cache.head_dim):
+        raise ValueError(f"q is for {B} sequences and head dim {D}, the cache for {cache.batch} and {cache.head_dim}")
+    _expect(q, "q", q.shape, torch.float16, torch.bfloat16)
+    _expect(out, "out", q.shape, torch.float32, torch.float16, torch.bfloat16)
+    _expect(lse, "lse", (B, n_q, n_q_heads), torch.float32)
+    _expect(seq_len, "seq_len", (B,), torch.int32)
+    _expect(q_len, "q_len", (B,), torch.int32)
+    _expect(slopes, "slopes", (n_q_heads,), torch.float32)
+    return B, n_q, n_q_heads
+
+
+def attn_scored_workspace(cache: PackedCache, max_seq_len: int, n_q: int, n_q_heads: int, n_split: int = 0) -> int:
+    return int(load().ckv_attn_scored_workspace(cache.ref(), max_seq_len, n_q, n_q_heads, n_split))
+
+
+def attn_scored(cache: PackedCache, seq_len, max_seq_len: int, q, scale: float, out, lse, workspace,
+                softcap: float = 0.0, window: int = 0, slopes=None, prefix_len=None, doc_start=None, q_len=None,
+                n_split: int = 0, stream=None):
+    """Attention of the newest n_q positions (q_len[b] of them when given) of every sequence, with a tanh
+    cap, a distance bias (slopes float32 [n_q_heads]), a sliding window, a prefix mask (prefix_len int32
+    [batch]) and a document mask (doc_start int32 [batch, n_q]). q: fp16 or bf16 [batch, n_q, n_q_heads, D];
+    out: float32, fp16 or bf16 like q; lse float32 [batch, n_q, n_q_heads]."""
+    import torch
+    B, n_q, n_q_heads = _scored_tensors(cache, seq_len, q, out, lse, q_len, slopes)
+    _expect(prefix_len, "prefix_len", (B,), torch.int32)
+    _expect(doc_start, "doc_start", (B, n_q), torch.int32)
+    score = CkvScoreStruct(softcap, window, _ptr(slopes), _ptr(prefix_len), _ptr(doc_start))
+    _check(load().ckv_attn_scored(cache.ref(), _ptr(seq_len), max_seq_len, _ptr(q), _dtype_code(q, "q"), n_q,
+                                  n_q_heads, _ptr(q_len), scale, ctypes.byref(score), n_split, _ptr(out),
+                                  _dtype_code(out, "out"), _ptr(lse), _ptr(workspace), workspace.numel(),
+                                  _stream(stream)))
+
+
+def attn_tree_workspace(cache: PackedCache, max_seq_len: int, n_q: int, n_q_heads: int, n_split: int = 0) -> int:
+    return int(load().ckv_attn_tree_workspace(cache.ref(), max_seq_len, n_q, n_q_heads, n_split))
+
+
+def attn_tree(cache: PackedCache, seq_len, max_seq_len: int, tree_mask, q, scale: float, out, lse, workspace,
+              softcap: float = 0.0, window: int = 0, slopes=None, q_len=None, n_split: int = 0, stream=None):
+    """Attention of a tree of drafted tokens, the newest n_q (or q_len[b]) positions of every sequence: node t
+    sees the committed cache and the nodes whose bits are set in tree_mask[b, t] (int64 or uint64 [batch, n_q],
+    its ancestors and itself). Tensors as attn_scored."""
+    import torch
+    B, n_q, n_q_heads = _scored_tensors(cache, seq_len, q, out, lse, q_len, slopes)
+    _expect(tree_mask, "tree_mask", (B, n_q), torch.int64, torch.uint64)
+    score = CkvScoreStruct(softcap, window, _ptr(slopes), None, None)
+    _check(load().ckv_attn_tree(cache.ref(), _ptr(seq_len), max_seq_len, _ptr(tree_mask), _ptr(q),
+                                _dtype_code(q, "q"), n_q, n_q_heads, _ptr(q_len), scale, ctypes.byref(score), n_split,
+                                _ptr(out), _dtype_code(out, "out"), _ptr(lse), _ptr(workspace), workspace.numel(),
+                                _stream(stream)))
+
+
+def tree_accept(cache: PackedCache, seq_len, n_q: int, path, path_len, new_len, q_len=None, flag=None, stream=None):
+    """Move the accepted nodes path[b, :path_len[b]] (int32 [batch, max_path]) of every sequence's drafted tree to
+    the front of its drafted positions, bit for bit, and store the new lengths in new_len (int32 [batch], not
+    seq_len itself). flag: int32 [1], set to 2 by an entry out of range."""
+    import torch
+    B = cache.batch
+    for t, what in ((seq_len, "seq_len"), (path_len, "path_len"), (new_len, "new_len"), (q_len, "q_len")):
+        _expect(t, what, (B,), torch.int32)
+    _expect(path, "path", (B, path.shape[-1]), torch.int32)
+    _expect(flag, "flag", (1,), torch.int32)
+    _check(load().ckv_tree_accept(cache.ref(), _ptr(seq_len), n_q, _ptr(q_len), _ptr(path), path.shape[-1],
+                                  _ptr(path_len), _ptr(new_len), _ptr(flag), _stream(stream)))
 
 
 def selftest_bounded_waits(workspace, stream=None):

@@ -11,6 +11,7 @@
 
 #include "../../include/ckv.h"
 #include "ckv_kernels.cuh"
+#include "scored.cuh"
 
 namespace {
 
@@ -907,6 +908,180 @@ ckv_status ckv_read_device_flag(const void* workspace, int32_t* flag, void* stre
     if (e != cudaSuccess) return cuda_fail(e, "flag clear");
     return fail(CKV_ERR_DEVICE_FLAG, "device flag %d", *flag);
   }
+  return CKV_OK;
+}
+
+// ------------------------------------------- attn_scored, attn_tree, tree_accept --
+
+// Splits of an attn_scored / attn_tree call: the sequence's keys are those
+// that a row can see, which a window bounds on the host.
+static ckv_status plan_scored(const ckv_cache* cache, int64_t max_seq_len, int n_q, int n_q_heads, int64_t keys,
+                              int n_split, DecodePlan* p) {
+  ckv_status s = plan_decode(cache->head_dim, cache->n_kv_heads, cache->batch, max_seq_len, n_q, n_q_heads, n_split, p);
+  if (s != CKV_OK) return s;
+  if (static_cast<int64_t>(cache->batch) * cache->n_kv_heads > 65535)
+    return fail(CKV_ERR_UNSUPPORTED, "batch * n_kv_heads above 65535");
+  if (!n_split) p->n_split = auto_split(p->groups, keys, cache->head_dim == 512 ? 4 : 8);
+  p->ws = p->n_split == 1 ? ws_header_bytes(p->groups, 1) : decode_ws_bytes(cache->head_dim, p->groups, p->n_split);
+  return CKV_OK;
+}
+
+size_t ckv_attn_scored_workspace(const ckv_cache* cache, int64_t max_seq_len, int32_t n_q, int32_t n_q_heads,
+                                 int32_t n_split) {
+  DecodePlan p;
+  if (check_cache(cache) != CKV_OK ||
+      plan_scored(cache, max_seq_len, n_q, n_q_heads, max_seq_len, n_split, &p) != CKV_OK)
+    return 0;
+  return p.ws;
+}
+
+static ckv_status run_scored(const ckv_cache* cache, const int32_t* seq_len, int64_t max_seq_len, const void* q,
+                             int32_t q_type, int32_t n_q, int32_t n_q_heads, const int32_t* q_len,
+                             const uint64_t* tree, float scale, const ckv_score* score, int32_t n_split, void* out,
+                             int32_t out_type, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  ckv_status s = check_cache(cache);
+  if (s != CKV_OK) return s;
+  const ckv_score none{};
+  if (!score) score = &none;
+  if (q_type != CKV_F16 && q_type != CKV_BF16) return fail(CKV_ERR_INVALID_ARG, "q_type must be CKV_F16 or CKV_BF16");
+  if (out_type != CKV_F32 && out_type != CKV_F16 && out_type != CKV_BF16)
+    return fail(CKV_ERR_INVALID_ARG, "out_type must be CKV_F32, CKV_F16 or CKV_BF16");
+  if (!std::isfinite(score->softcap) || score->softcap < 0.0f)
+    return fail(CKV_ERR_INVALID_ARG, "softcap must be finite and not negative (0: none)");
+  if (score->window < 0) return fail(CKV_ERR_INVALID_ARG, "window negative (0: none)");
+  if (max_seq_len > 0x7fffffffLL - 64) return fail(CKV_ERR_UNSUPPORTED, "max_seq_len above 2^31 - 65");
+  int64_t keys = max_seq_len;
+  if (score->window && !score->prefix_len && keys > (int64_t)score->window + n_q) keys = (int64_t)score->window + n_q;
+  DecodePlan p;
+  s = plan_scored(cache, max_seq_len, n_q, n_q_heads, keys, n_split, &p);
+  if (s != CKV_OK) return s;
+  if (!seq_len || !q || !out || !lse) return fail(CKV_ERR_INVALID_ARG, "null seq_len/q/out/lse");
+  if (!aligned(q, 16) || !aligned(out, 16)) return fail(CKV_ERR_INVALID_ARG, "q/out must be 16-byte aligned");
+  if (!aligned(seq_len, 4) || !aligned(lse, 4) || !aligned(q_len, 4) || !aligned(tree, 8) ||
+      !aligned(score->slopes, 4) || !aligned(score->prefix_len, 4) || !aligned(score->doc_start, 4))
+    return fail(CKV_ERR_INVALID_ARG, "misaligned lengths, masks or slopes");
+  if (!std::isfinite(scale)) return fail(CKV_ERR_INVALID_ARG, "scale not finite");
+  s = check_ws(ws, ws_bytes, p.ws);
+  if (s != CKV_OK) return s;
+  const ckv::MergeTree tr = ckv::merge_tree(p.n_split);
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  ckv::ScoredArgs a{};
+  a.cache = static_cast<const uint8_t*>(cache->data);
+  a.signs = cache->v_signs;
+  a.signs2 = cache->v_signs2;
+  a.rot = cache->v_signs2 ? 1 : 0;
+  a.capacity = cache->capacity;
+  a.head_dim = cache->head_dim;
+  a.n_kv_heads = cache->n_kv_heads;
+  a.batch = cache->batch;
+  a.v_bits = cache_v_bits(cache);
+  a.seq_len = seq_len;
+  a.max_seq_len = max_seq_len;
+  a.q = static_cast<const __half*>(q);
+  a.q_bf16 = q_type == CKV_BF16;
+  a.n_q = n_q;
+  a.n_q_heads = n_q_heads;
+  a.n_split = p.n_split;
+  a.n_row_groups = p.n_row_groups;
+  a.part = reinterpret_cast<float*>(base + ws_header_bytes(p.groups, p.n_split));
+  a.sub = a.part + static_cast<size_t>(p.groups) * p.n_split * ckv::merge_slot_floats(cache->head_dim);
+  a.merge_ls = tr.ls;
+  a.merge_nl = tr.nl;
+  a.sub_stride = tr.nl;
+  a.ctr_stride = ctr_stride(p.n_split);
+  a.flag = reinterpret_cast<int32_t*>(base);
+  a.counters = reinterpret_cast<uint32_t*>(base + 64);
+  a.out = static_cast<float*>(out);
+  a.out_type = out_type;
+  a.lse = lse;
+  a.q_len = q_len;
+  a.tree = tree;
+  a.slopes = score->slopes;
+  a.prefix_len = score->prefix_len;
+  a.doc_start = score->doc_start;
+  a.window = score->window;
+  // The products carry 2^-24 (the codes enter the tensor cores as subnormals).
+  constexpr float kLog2e = 1.4426950408889634f, kCodes = 16777216.0f;
+  a.cap_log2 = score->softcap * kLog2e;
+  a.mul = score->softcap > 0.0f ? scale * kCodes / score->softcap : scale * kCodes * kLog2e;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = a.v_bits == 2   ? ckv::launch_scored_mma2(a, st)
+                        : a.v_bits == 4 ? ckv::launch_scored_mma4(a, st)
+                                        : ckv::launch_scored_mma3(a, st);
+  if (e != cudaSuccess) return cuda_fail(e, "scored attention launch");
+  return CKV_OK;
+}
+
+ckv_status ckv_attn_scored(const ckv_cache* cache, const int32_t* seq_len, int64_t max_seq_len, const void* q,
+                           int32_t q_type, int32_t n_q, int32_t n_q_heads, const int32_t* q_len, float scale,
+                           const ckv_score* score, int32_t n_split, void* out, int32_t out_type, float* lse,
+                           void* workspace, size_t ws_bytes, void* stream) {
+  return run_scored(cache, seq_len, max_seq_len, q, q_type, n_q, n_q_heads, q_len, nullptr, scale, score, n_split, out,
+                    out_type, lse, workspace, ws_bytes, stream);
+}
+
+static ckv_status check_nodes(int32_t n_q) {
+  if (n_q < 1 || n_q > 64) return fail(CKV_ERR_UNSUPPORTED, "a tree has 1 to 64 nodes (n_q = %d)", n_q);
+  return CKV_OK;
+}
+
+size_t ckv_attn_tree_workspace(const ckv_cache* cache, int64_t max_seq_len, int32_t n_q, int32_t n_q_heads,
+                               int32_t n_split) {
+  return check_nodes(n_q) == CKV_OK ? ckv_attn_scored_workspace(cache, max_seq_len, n_q, n_q_heads, n_split) : 0;
+}
+
+ckv_status ckv_attn_tree(const ckv_cache* cache, const int32_t* seq_len, int64_t max_seq_len,
+                         const uint64_t* tree_mask, const void* q, int32_t q_type, int32_t n_q, int32_t n_q_heads,
+                         const int32_t* q_len, float scale, const ckv_score* score, int32_t n_split, void* out,
+                         int32_t out_type, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  ckv_status s = check_nodes(n_q);
+  if (s != CKV_OK) return s;
+  if (!tree_mask) return fail(CKV_ERR_INVALID_ARG, "tree_mask is null");
+  if (score && (score->prefix_len || score->doc_start))
+    return fail(CKV_ERR_INVALID_ARG, "a tree takes no prefix or document mask");
+  return run_scored(cache, seq_len, max_seq_len, q, q_type, n_q, n_q_heads, q_len, tree_mask, scale, score, n_split,
+                    out, out_type, lse, workspace, ws_bytes, stream);
+}
+
+ckv_status ckv_tree_accept(const ckv_cache* cache, const int32_t* seq_len, int32_t n_q, const int32_t* q_len,
+                           const int32_t* path, int32_t max_path, const int32_t* path_len, int32_t* new_len,
+                           int32_t* flag, void* stream) {
+  ckv_status s = check_cache(cache);
+  if (s == CKV_OK) s = check_nodes(n_q);
+  if (s != CKV_OK) return s;
+  if (max_path < 1 || max_path > 64) return fail(CKV_ERR_UNSUPPORTED, "a path has 1 to 64 nodes (max_path = %d)", max_path);
+  if (cache->batch > 65535) return fail(CKV_ERR_UNSUPPORTED, "batch above 65535");
+  if (!seq_len || !path || !path_len || !new_len) return fail(CKV_ERR_INVALID_ARG, "null seq_len/path/path_len/new_len");
+  if (!aligned(seq_len, 4) || !aligned(q_len, 4) || !aligned(path, 4) || !aligned(path_len, 4) || !aligned(new_len, 4) ||
+      !aligned(flag, 4))
+    return fail(CKV_ERR_INVALID_ARG, "misaligned lengths or paths");
+  // The kernel writes new_len while other CTAs still read the lengths and paths.
+  const uintptr_t w0 = reinterpret_cast<uintptr_t>(new_len), w1 = w0 + 4u * static_cast<uintptr_t>(cache->batch);
+  auto overlaps = [&](const void* p, size_t n) {
+    const uintptr_t r0 = reinterpret_cast<uintptr_t>(p);
+    return p && r0 < w1 && w0 < r0 + 4u * n;
+  };
+  const size_t B = static_cast<size_t>(cache->batch);
+  if (overlaps(seq_len, B) || overlaps(q_len, B) || overlaps(path_len, B) || overlaps(path, B * max_path))
+    return fail(CKV_ERR_INVALID_ARG, "new_len overlaps an input");
+  ckv::AcceptArgs a{};
+  a.cache = static_cast<uint8_t*>(cache->data);
+  a.capacity = cache->capacity;
+  a.head_dim = cache->head_dim;
+  a.n_kv_heads = cache->n_kv_heads;
+  a.batch = cache->batch;
+  a.v_bits = cache_v_bits(cache);
+  a.rot = cache->v_signs2 ? 1 : 0;
+  a.seq_len = seq_len;
+  a.n_q = n_q;
+  a.q_len = q_len;
+  a.path = path;
+  a.max_path = max_path;
+  a.path_len = path_len;
+  a.new_len = new_len;
+  a.flag = flag;
+  const cudaError_t e = ckv::launch_tree_accept(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "tree_accept launch");
   return CKV_OK;
 }
 

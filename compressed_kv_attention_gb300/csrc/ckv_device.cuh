@@ -72,6 +72,9 @@ enum DeviceFlag : int32_t {
   kFlagInternal = 3,      // a work schedule the kernel cannot run (a library bug)
 };
 
+// Types of an output row (the values of ckv_dtype in the public header).
+enum OutType : int { kOutF32 = 0, kOutF16 = 1, kOutBf16 = 2 };
+
 // ------------------------------------------------------------------- misc --
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -236,6 +239,12 @@ __device__ __forceinline__ uint32_t hmul2_u32(uint32_t x, uint32_t y) {
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf162(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 

@@ -91,6 +91,7 @@ struct DecodeArgs {
   uint32_t* counters;        // ctr_stride words per group, zero between calls
   int ctr_stride;
   float* out;
+  int out_type;              // OutType of the rows at `out` (attn_scored, attn_tree; the other decodes write fp32)
   float* lse;
   // Append (compressed decode, one row group): before its tiles are read, the
   // CTA that owns positions [seq_len - n_new, seq_len) of a sequence and kv
@@ -141,6 +142,22 @@ struct F16AppendArgs {
   int64_t token_stride, batch_stride;  // in elements
 };
 cudaError_t launch_f16_append(const F16AppendArgs& a, cudaStream_t stream);
+
+// The accepted path of a drafted tree moved to the front of its positions.
+struct AcceptArgs {
+  uint8_t* cache;
+  int64_t capacity;
+  int head_dim, n_kv_heads, batch, v_bits, rot;
+  const int32_t* seq_len;
+  int n_q;
+  const int32_t* q_len;         // nodes per sequence or nullptr: n_q
+  const int32_t* path;          // [batch][max_path]
+  int max_path;
+  const int32_t* path_len;
+  int32_t* new_len;
+  int32_t* flag;                // or nullptr
+};
+cudaError_t launch_tree_accept(const AcceptArgs& a, cudaStream_t stream);
 
 struct LseMergeArgs {
   const float* o[16];

@@ -155,6 +155,20 @@ __device__ __forceinline__ void exchange_S(float (&S)[4], float4* xbuf, int grou
   xchg_get<WT>(S, xbuf, group, parity, lane);
 }
 
+// Output rows are fp32 in the plain decodes. With ANY (attn_scored, attn_tree)
+// they have the type of out_type (kOutF32 / kOutF16 / kOutBf16) and travel as
+// opaque float pointers: the store converts, one rounding per value.
+template <bool ANY>
+__device__ __forceinline__ void store_out2(float* row, int pair, float2 v, int out_type) {
+  if (ANY && out_type == kOutF16) {
+    reinterpret_cast<uint32_t*>(row)[pair] = pack_half2(v.x, v.y);
+  } else if (ANY && out_type == kOutBf16) {
+    reinterpret_cast<uint32_t*>(row)[pair] = pack_bf162(v.x, v.y);
+  } else {
+    reinterpret_cast<float2*>(row)[pair] = v;
+  }
+}
+
 // Inverse rotation of one output row held by a warp (lane: dims 64 e + 2 lane
 // + c, c < 2), then the sign flip and vscale / D, stored to `orow`:
 // the unnormalised Walsh-Hadamard transform pairs the two values of a float2
@@ -165,10 +179,10 @@ __device__ __forceinline__ void exchange_S(float (&S)[4], float4* xbuf, int grou
 // ROT = 1 (block-diagonal rotation): the second diagonal `signs2` comes first,
 // the butterfly stays inside 128-dim groups (the register stages stop at dim
 // bit 6), and the scale is vscale / 128 (the norms were applied to V itself).
-template <int D, int ROT = 0>
+template <int D, int ROT = 0, bool ANY = false>
 __device__ __forceinline__ void derotate_store_row(float2 (&v)[D / 64], int lane, const int8_t* signs,
                                                    float* orow, float vscale = kCentroidScale,
-                                                   const int8_t* signs2 = nullptr) {
+                                                   const int8_t* signs2 = nullptr, int out_type = kOutF32) {
   constexpr int E2 = D / 64;
   constexpr int EG = ROT ? kRotGroup / 64 : E2;   // register stages inside one transform group
   constexpr float GSCALE = ROT ? 1.0f / kRotGroup : 1.0f / D;
@@ -216,9 +230,8 @@ __device__ __forceinline__ void derotate_store_row(float2 (&v)[D / 64], int lane
     }
   }
   if (orow) {
-    float2* o2 = reinterpret_cast<float2*>(orow) + lane;
 #pragma unroll
-    for (int e = 0; e < E2; ++e) o2[32 * e] = v[e];
+    for (int e = 0; e < E2; ++e) store_out2<ANY>(orow, lane + 32 * e, v[e], out_type);
   }
 }
 
@@ -237,19 +250,21 @@ __device__ __forceinline__ void derotate_store_row(float2 (&v)[D / 64], int lane
 // Each group stores its unscaled accumulators with its own (m, l); warp r < 8
 // owns row r and rescales the groups while summing them (other warps are done
 // after the second barrier).
+template <bool ANY = false>
 __device__ __forceinline__ void row_outputs(const DecodeArgs& a, int b, int kvh, int rg, int r, float** o,
                                             float** l);
 
 // With `direct` (a launch of one split and nothing to merge) the rows go
 // straight to the outputs of row group (b, kvh, rg), normalised, with their
-// lse, instead of to the slot.
-template <typename Sh, int MTW, int ROT = 0>
+// lse, instead of to the slot. The row states come from the warp wh = owner
+// of each tile group.
+template <typename Sh, int MTW, int ROT = 0, bool ANY = false>
 __device__ __forceinline__ void decode_epilogue(SoftmaxState st, float (&acc)[MTW][4], float* red,
                                                 float* mlbuf, int group, int wh, int warp, int lane,
                                                 const int8_t* signs, float* slot,
                                                 float vscale = kCentroidScale, const int8_t* signs2 = nullptr,
                                                 const DecodeArgs* direct = nullptr, int b = 0, int kvh = 0,
-                                                int rg = 0) {
+                                                int rg = 0, int owner = 0) {
   constexpr int D = Sh::DIM;
   const int g = lane >> 2, t = lane & 3;
   // Reduce the row sums over the 8 lanes that share rows (2t, 2t+1).
@@ -260,7 +275,7 @@ __device__ __forceinline__ void decode_epilogue(SoftmaxState st, float (&acc)[MT
   st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, 8);
   st.l1 += __shfl_xor_sync(0xffffffffu, st.l1, 16);
   named_bar(1, Sh::NCW * 32);  // every consumer is done with the stage memory
-  if (wh == 0 && lane < 4) {
+  if (wh == owner && lane < 4) {
     mlbuf[group * 16 + (2 * t) * 2 + 0] = st.m0;
     mlbuf[group * 16 + (2 * t) * 2 + 1] = st.l0;
     mlbuf[group * 16 + (2 * t + 1) * 2 + 0] = st.m1;
@@ -307,12 +322,12 @@ __device__ __forceinline__ void decode_epilogue(SoftmaxState st, float (&acc)[MT
   if (direct) {
     float* orow;
     float* lrow;
-    row_outputs(*direct, b, kvh, rg, r, &orow, &lrow);
+    row_outputs<ANY>(*direct, b, kvh, rg, r, &orow, &lrow);
     if (!orow) return;
     const float inv = lc > 0.0f ? 1.0f / lc : 0.0f;
 #pragma unroll
     for (int e = 0; e < E2; ++e) v[e] = make_float2(v[e].x * inv, v[e].y * inv);
-    derotate_store_row<D, ROT>(v, lane, signs, orow, vscale, signs2);
+    derotate_store_row<D, ROT, ANY>(v, lane, signs, orow, vscale, signs2, ANY ? direct->out_type : kOutF32);
     if (lane == 0) *lrow = lc > 0.0f ? (mc + log2f(lc)) * 0.6931471805599453f : -INFINITY;
     return;
   }
@@ -413,6 +428,7 @@ __device__ __forceinline__ void load_q_frags(uint32_t (&qf)[NBW][4], const __hal
 
 
 // Output pointers of the 8 rows of row group `rg` (nullptr for padding rows).
+template <bool ANY>
 __device__ __forceinline__ void row_outputs(const DecodeArgs& a, int b, int kvh, int rg, int r,
                                             float** o, float** l) {
   const int group_q = a.n_q_heads / a.n_kv_heads;
@@ -425,7 +441,9 @@ __device__ __forceinline__ void row_outputs(const DecodeArgs& a, int b, int kvh,
   int qi, h;
   row_to_query(rr, group_q, kvh, qi, h);
   const int64_t orow = (int64_t)(b * a.n_q + qi) * a.n_q_heads + h;
-  *o = a.out + orow * a.head_dim;
+  *o = (ANY && a.out_type != kOutF32)
+           ? reinterpret_cast<float*>(reinterpret_cast<uint16_t*>(a.out) + orow * a.head_dim)
+           : a.out + orow * a.head_dim;
   *l = a.lse + orow;
 }
 
@@ -554,7 +572,7 @@ __device__ __forceinline__ bool merge_slots(const float* src, int cnt, uint8_t* 
 // Tree merge, after the epilogue has written this CTA's slot: count into the
 // leaf and, when this CTA completes the leaf (and then the root), merge. 256
 // consumer threads, named barrier 1. `scratch` (SCR bytes) is the stage memory.
-template <int D, int SCR>
+template <int D, int SCR, bool ANY = false>
 __device__ __forceinline__ void tree_merge_tail(const DecodeArgs& a, int split, int64_t gid, int b, int kvh,
                                                 int rg, int tid, uint8_t* scratch) {
   constexpr int64_t SLOT = merge_slot_floats(D);
@@ -614,7 +632,7 @@ __device__ __forceinline__ void tree_merge_tail(const DecodeArgs& a, int split, 
       __threadfence();
     }
   }
-  if (tid < 8) row_outputs(a, b, kvh, rg, tid, &s_out[tid], &s_lse[tid]);
+  if (tid < 8) row_outputs<ANY>(a, b, kvh, rg, tid, &s_out[tid], &s_lse[tid]);
   named_bar(1, 256);
   if (!s_last) return;
 
@@ -639,7 +657,7 @@ __device__ __forceinline__ void tree_merge_tail(const DecodeArgs& a, int split, 
     float2 v[D / 64];
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) v[e] = reinterpret_cast<const float2*>(rows + r * D)[32 * e + lane];
-    derotate_store_row<D>(v, lane, nullptr, s_out[r]);
+    derotate_store_row<D, 0, ANY>(v, lane, nullptr, s_out[r], kCentroidScale, nullptr, ANY ? a.out_type : kOutF32);
     if (lane == 0 && s_lse[r]) {
       const float L = s_L[r];
       *s_lse[r] = (L > 0.0f) ? (s_M[r] + log2f(L)) * 0.6931471805599453f : -INFINITY;
@@ -665,11 +683,11 @@ __device__ __forceinline__ uint32_t ld_acquire_u32(const uint32_t* p) {
 // reduced by all threads at once (the (m, l) entries a thread holds all belong
 // to row tid % 8); each output unit is summed by k consecutive lanes and
 // reduced with shuffles.
-template <int D>
+template <int D, bool ANY = false>
 __device__ __forceinline__ void merge_slice(const float* slots, int n_split, int u0, int u1, int tid, int nthr,
                                             float* sm, float* const* out_rows, float* const* lse_rows,
                                             bool write_lse, int bar_id, const float* extra = nullptr,
-                                            int n_extra = 1) {
+                                            int n_extra = 1, int out_type = kOutF32) {
   constexpr int U = D / 4;                               // float4 units per row
   constexpr int64_t SLOT = merge_slot_floats(D);
   constexpr int MLR = 4;                                 // (m, l) pairs per thread in registers
@@ -801,11 +819,17 @@ __device__ __forceinline__ void merge_slice(const float* slots, int n_split, int
       float L = 0.0f;
       for (int ww = 0; ww < nw; ++ww) L += wsum[ww * 8 + r];
       const float inv = (L > 0.0f) ? 1.0f / L : 0.0f;
-      float* o = out_rows[r] + 4 * ((u0 + el) % U);
-      o[0] = acc.x * inv;
-      o[1] = acc.y * inv;
-      o[2] = acc.z * inv;
-      o[3] = acc.w * inv;
+      if constexpr (ANY) {
+        const int pair = 2 * ((u0 + el) % U);
+        store_out2<true>(out_rows[r], pair, make_float2(acc.x * inv, acc.y * inv), out_type);
+        store_out2<true>(out_rows[r], pair + 1, make_float2(acc.z * inv, acc.w * inv), out_type);
+      } else {
+        float* o = out_rows[r] + 4 * ((u0 + el) % U);
+        o[0] = acc.x * inv;
+        o[1] = acc.y * inv;
+        o[2] = acc.z * inv;
+        o[3] = acc.w * inv;
+      }
     }
   }
 }
@@ -815,7 +839,7 @@ __device__ __forceinline__ void merge_slice(const float* slots, int n_split, int
 // shared floats). The wait is bounded: on timeout the device flag is raised
 // and the CTA leaves without merging (the counters are then left non-zero: a
 // workspace whose flag was raised is zeroed before reuse).
-template <int D, int NT>
+template <int D, int NT, bool ANY = false>
 __device__ __forceinline__ void rendezvous_merge_tail(const DecodeArgs& a, int split, int64_t gid, int b, int kvh,
                                                       int rg, int tid, float* scratch) {
   __shared__ int s_ok;
@@ -857,7 +881,7 @@ __device__ __forceinline__ void rendezvous_merge_tail(const DecodeArgs& a, int s
       s_out[tid] = a.fold_out + orow * a.head_dim;
       s_lse[tid] = a.fold_lse + orow;
     } else {
-      row_outputs(a, b, kvh, rg, tid, &s_out[tid], &s_lse[tid]);
+      row_outputs<ANY>(a, b, kvh, rg, tid, &s_out[tid], &s_lse[tid]);
     }
   }
   named_bar(1, NT);
@@ -872,8 +896,8 @@ __device__ __forceinline__ void rendezvous_merge_tail(const DecodeArgs& a, int s
     extra = a.ext_part + ((int64_t)kvh * a.ext_nrg + b) * a.ext_n * merge_slot_floats(D);
     n_extra = a.ext_n;
   }
-  merge_slice<D>(a.part + mg * nm * merge_slot_floats(D), nm, u0, u1, tid, NT, scratch, s_out, s_lse, cm == 0, 1,
-                 extra, n_extra);
+  merge_slice<D, ANY>(a.part + mg * nm * merge_slot_floats(D), nm, u0, u1, tid, NT, scratch, s_out, s_lse, cm == 0, 1,
+                      extra, n_extra, ANY ? a.out_type : kOutF32);
   if (tid == 0 && dep + 1 == n) {  // the last CTA to leave: nobody reads the counters any more
     *arrive = 0u;
     *depart = 0u;
@@ -883,13 +907,13 @@ __device__ __forceinline__ void rendezvous_merge_tail(const DecodeArgs& a, int s
 // The split merge after the epilogue: rendezvous when the host found the grid
 // co-resident (on all NT consumer threads), else the tree (on threads < 256;
 // the others leave).
-template <int D, int SCR, int NT>
+template <int D, int SCR, int NT, bool ANY = false>
 __device__ __forceinline__ void decode_split_tail(const DecodeArgs& a, int split, int64_t gid, int b, int kvh,
                                                   int rg, int tid, uint8_t* scratch) {
   if (a.rendezvous) {
-    rendezvous_merge_tail<D, NT>(a, split, gid, b, kvh, rg, tid, reinterpret_cast<float*>(scratch));
+    rendezvous_merge_tail<D, NT, ANY>(a, split, gid, b, kvh, rg, tid, reinterpret_cast<float*>(scratch));
   } else if (tid < 256) {
-    tree_merge_tail<D, SCR>(a, split, gid, b, kvh, rg, tid, scratch);
+    tree_merge_tail<D, SCR, ANY>(a, split, gid, b, kvh, rg, tid, scratch);
   }
 }
 
@@ -923,10 +947,12 @@ struct ResidencyCache {
 // device (ckv_set_concurrent_kernels), a grid that fits may still not be
 // resident all at once, so the tree merge, which never waits for another
 // CTA, is used instead.
-template <typename K>
-static inline cudaError_t launch_split_decode(K kernel, DecodeArgs a, int threads, size_t smem, ResidencyCache* cache,
-                                              cudaStream_t stream) {
-  const int64_t grid_total = (int64_t)a.n_split * a.n_row_groups * a.batch * a.n_kv_heads;
+// groups_per_cta: row groups that one CTA carries (attn_scored, attn_tree).
+template <typename K, typename Args>
+static inline cudaError_t launch_split_decode(K kernel, Args a, int threads, size_t smem, ResidencyCache* cache,
+                                              cudaStream_t stream, int groups_per_cta = 1) {
+  const int grid_y = (a.n_row_groups + groups_per_cta - 1) / groups_per_cta;
+  const int64_t grid_total = (int64_t)a.n_split * grid_y * a.batch * a.n_kv_heads;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) dev = 0;
   if (cache->blocks[dev] == 0) cache->blocks[dev] = coresident_blocks(kernel, threads, smem);
@@ -937,7 +963,7 @@ static inline cudaError_t launch_split_decode(K kernel, DecodeArgs a, int thread
   if (!a.rendezvous) a.dca_fold = 0;
   if (a.host_folded) *a.host_folded = a.dca_fold;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.n_split, a.n_row_groups, a.batch * a.n_kv_heads);
+  cfg.gridDim = dim3(a.n_split, grid_y, a.batch * a.n_kv_heads);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

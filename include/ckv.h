@@ -33,7 +33,7 @@
  *    a multiple of the number of KV heads; query head h reads KV head
  *    floor(h / G), G = n_q_heads / n_kv_heads (grouped-query attention, as the
  *    Upstream Sync page's entry 0080 describes for Gemma-4: 16 heads, 2 KV heads).
- *  - Outputs are float32: the normalised attention output and the natural-log
+ *  - Outputs are float32 (attn_scored and attn_tree take a type): the normalised attention output and the natural-log
  *    log-sum-exp of every query row, the "FA output packed with per-row LSE"
  *    contract of the DCA page ("Feature — Gemma-4 A4B Dual Chunk Attention (DCA),
  *    training-free 1M context", section "Implementation progress + Section-D
@@ -575,6 +575,98 @@ CKV_API ckv_status ckv_attn_prefill_shared(const ckv_cache* prefix, int64_t n_pr
                                    const void* v_new_f16, int32_t n_new, int32_t n_q_heads,
                                    float scale, float* out, float* lse, void* workspace,
                                    size_t ws_bytes, void* stream);
+
+/* Element types of the queries and outputs of attn_scored and attn_tree. */
+typedef enum { CKV_F32 = 0, CKV_F16 = 1, CKV_BF16 = 2 } ckv_dtype;
+
+/*
+ * Score modifications and masks of attn_scored and attn_tree; a zero-filled
+ * struct (or a NULL pointer to it) means none. For a query at position i and a
+ * key at position p, with s = scale * q.k:
+ *   softcap c > 0:  s becomes c * tanh(s / c);
+ *   slopes:         then s - slopes[h] * |i - p| (a bias that falls with distance);
+ *   window w > 0:   p is visible only when i - p < w;
+ *   prefix_len:     prefix mask: positions below prefix_len[b] (at most the
+ *                   sequence's length) are visible to earlier queries too;
+ *   doc_start:      document mask: query token t sees no position below
+ *                   doc_start[b][t] (also the left padding of a batch).
+ * No counterpart in the pages: their attention has no softcap, bias or window.
+ */
+typedef struct {
+  float softcap;             /* finite, >= 0; 0: none */
+  int32_t window;            /* >= 0; 0: none */
+  const float* slopes;       /* NULL, or device float32 [n_q_heads], finite */
+  const int32_t* prefix_len; /* NULL, or device int32 [batch] (attn_scored) */
+  const int32_t* doc_start;  /* NULL, or device int32 [batch][n_q] (attn_scored) */
+} ckv_score;
+
+/*
+ * attn_scored — attention of the n newest positions of every sequence over the
+ * packed cache, with the modifications of ckv_score: one token, a verify batch
+ * or a prompt whose rows kv_pack has written. n = n_q, or q_len[b] (device,
+ * [batch], each in [0, n_q]; NULL: n_q): query token t < n is at position
+ * i = seq_len[b] - n + t and sees the positions
+ *   [max(0, doc_start, i - window + 1), max(i + 1, min(prefix_len, seq_len))).
+ * A token before position 0 (a sequence shorter than its queries) and the
+ * tokens t >= n are rows that see nothing: output 0, lse -inf.
+ * q: device [batch][n_q][n_q_heads][D] of q_type CKV_F16 or CKV_BF16 (bf16 is
+ * converted to fp16, exact within fp16's range). out: the same shape in
+ * out_type (any ckv_dtype), 16-byte aligned; lse float32 [batch][n_q][n_q_heads].
+ * n_split: 0 automatic, > 0 that many key splits.
+ * Workspace: ckv_attn_scored_workspace bytes (the same n_split), zero-filled
+ * once; one call at a time uses it, captured graphs included. A seq_len outside
+ * [0, min(capacity, max_seq_len)] or a q_len outside [0, n_q] makes every row
+ * of that sequence empty and raises the device flag (2).
+ * Errors: INVALID_ARG (null or misaligned pointers, types, a softcap that is
+ * negative or not finite, a negative window, a scale that is not finite),
+ * UNSUPPORTED (head dim, head ratio, more than 65535 (sequence, kv head) pairs
+ * or 524280 query rows per kv head), WORKSPACE.
+ */
+CKV_API size_t ckv_attn_scored_workspace(const ckv_cache* cache, int64_t max_seq_len, int32_t n_q,
+                                         int32_t n_q_heads, int32_t n_split);
+CKV_API ckv_status ckv_attn_scored(const ckv_cache* cache, const int32_t* seq_len, int64_t max_seq_len,
+                                   const void* q, int32_t q_type, int32_t n_q, int32_t n_q_heads,
+                                   const int32_t* q_len, float scale, const ckv_score* score, int32_t n_split,
+                                   void* out, int32_t out_type, float* lse, void* workspace, size_t ws_bytes,
+                                   void* stream);
+
+/*
+ * attn_tree — attn_verify for a tree of drafted tokens: the n nodes (n_q, or
+ * q_len[b]) are the newest n positions of the sequence (their K and V rows
+ * packed, their lengths counted), base = seq_len[b] - n. Node t sees every
+ * position below base and node j where bit j of tree_mask[b][t] is set (its
+ * ancestors and itself; bits from n on are ignored). Its position, for the
+ * window and the bias, is base + depth, depth = the number of its set bits
+ * - 1; drafted keys count by their own depth. tree_mask: device uint64
+ * [batch][n_q], 8-byte aligned. At most 64 nodes. A node with no bits over an
+ * empty cache sees nothing; n > seq_len[b] counts as out of range (flag 2).
+ * score: softcap, window and slopes (NULL prefix_len and doc_start). The other
+ * arguments, the errors and the workspace rules are attn_scored's.
+ */
+CKV_API size_t ckv_attn_tree_workspace(const ckv_cache* cache, int64_t max_seq_len, int32_t n_q,
+                                       int32_t n_q_heads, int32_t n_split);
+CKV_API ckv_status ckv_attn_tree(const ckv_cache* cache, const int32_t* seq_len, int64_t max_seq_len,
+                                 const uint64_t* tree_mask, const void* q, int32_t q_type, int32_t n_q,
+                                 int32_t n_q_heads, const int32_t* q_len, float scale, const ckv_score* score,
+                                 int32_t n_split, void* out, int32_t out_type, float* lse, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/*
+ * tree_accept — after an attn_tree step: the accepted nodes become the newest
+ * positions. In every kv head of sequence b, position base + path[b][j] is
+ * copied to base + j for j < path_len[b] (codes, scales and norms bit for bit;
+ * base = seq_len[b] - n, n = q_len[b] or n_q), and new_len[b] = base +
+ * path_len[b]. Every source is read before any target is written, so the path
+ * may have any order and repeat nodes. The positions from new_len[b] on keep
+ * their bytes. path: device int32 [batch][max_path], max_path <= 64; path_len,
+ * new_len: device int32 [batch]; new_len overlaps none of the inputs (give it
+ * to the next call as its seq_len). A sequence with a length, path length or
+ * path entry out of range keeps its cache and gets new_len = seq_len, and
+ * *flag (device int32, or NULL) is set to 2 if it was 0. No workspace.
+ */
+CKV_API ckv_status ckv_tree_accept(const ckv_cache* cache, const int32_t* seq_len, int32_t n_q,
+                                   const int32_t* q_len, const int32_t* path, int32_t max_path,
+                                   const int32_t* path_len, int32_t* new_len, int32_t* flag, void* stream);
 
 /*
  * set_concurrent_kernels — declare (on != 0) that other kernels may run on the
