@@ -181,7 +181,7 @@ __device__ __forceinline__ void q_block_bias(const uint32_t (&qf)[NBW][4], int l
 // A-fragment register k % 4 of m-tile k / 4.
 // ROT: nA / nB are the lane's group norms of positions (2t, 2t + 1) and
 // (2t + 8, 2t + 9) as fp16 pairs, multiplied into the A registers.
-template <int D, int B, int ROT>
+template <int D, int B, int ROT, bool PSPLIT = CDec<D, B, ROT>::PSPLIT>
 __device__ __forceinline__ void pv_tile(uint32_t rb, const uint8_t* lut, uint32_t lane4, int wh, int lane,
                                         uint32_t pb0, uint32_t pb1, const uint32_t (&pl)[2],
                                         float (&acc)[CDec<D, B, ROT>::MT_W][4], uint32_t nA, uint32_t nB) {
@@ -213,7 +213,7 @@ __device__ __forceinline__ void pv_tile(uint32_t rb, const uint8_t* lut, uint32_
       av[3] = hmul2_u32(av[3], nB);
     }
     mma16816(acc[i], av[0], av[1], av[2], av[3], pb0, pb1);
-    if constexpr (C::PSPLIT) mma16816(acc[i], av[0], av[1], av[2], av[3], pl[0], pl[1]);
+    if constexpr (PSPLIT) mma16816(acc[i], av[0], av[1], av[2], av[3], pl[0], pl[1]);
   }
 }
 

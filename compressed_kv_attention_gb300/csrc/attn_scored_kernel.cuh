@@ -1,22 +1,21 @@
-// attn_scored_kernel.cuh — attn_scored and attn_tree on mma.sync: the split-K
-// decode over the packed records with scored.cuh's masks and logits, for NR row
-// groups (8 NR query rows of one kv head) per CTA.
+// attn_scored_kernel.cuh — attn_scored and attn_tree with few query rows, on
+// mma.sync: the split-K decode over the packed records with scored.cuh's masks
+// and logits, one row group (8 query rows of one kv head) per CTA.
 //
 // Mathematics: the decode kernel's (S^T = K_hat Q^T and O^T += C^T P'^T, the
 // codes widened in registers, one online softmax over the row's keys), with
 // x = c tanh(mul S) - slope |distance| between the product and the softmax.
-// What the row groups share is the dequantised A side: a tile's K codes and V
-// centroids turn into fragments once and multiply every group's Q and P'.
 #pragma once
 
 #include "attn_decode_kernel.cuh"
+#include "attn_scored_tiles.cuh"
 #include "scored.cuh"
 
 namespace ckv {
 
 namespace {
 
-template <int D, int B, int ROT, int NR>
+template <int D, int B, int ROT>
 struct CScored : DecodeShape<D> {
   using Sh = DecodeShape<D>;
   static constexpr int NGRP = ROT ? D / kRotGroup : 1;
@@ -24,7 +23,9 @@ struct CScored : DecodeShape<D> {
   static constexpr int STAGE = Sh::NP * REC;
   static constexpr int NSTAGE = 4;
   static constexpr int THREADS = (Sh::NCW + 1) * 32;
-  static constexpr bool PSPLIT = CDec<D, B, ROT>::PSPLIT;
+  // The rotated tiers round V's fragments to fp16 once more (the group norms
+  // scale them), so their P' is always the fp16 pair.
+  static constexpr bool PSPLIT = ROT || D <= 128;
   static constexpr int LUT = CDec<D, B, ROT>::LUT;
   static constexpr int RED_BYTES = Sh::NP * Sh::RED_FLOATS * 4;
   static constexpr int RING = (NSTAGE * STAGE > RED_BYTES) ? NSTAGE * STAGE : RED_BYTES;
@@ -49,13 +50,12 @@ __device__ __forceinline__ void convert_q_frags(uint32_t (&qf)[NBW][4]) {
 
 }  // namespace
 
-template <int D, int B, int ROT, int NR>
-__global__ void __launch_bounds__(CScored<D, B, ROT, NR>::THREADS, 1) attn_scored_kernel(ScoredArgs a) {
-  static_assert(NR == 1, "one row group per CTA");
-  using C = CScored<D, B, ROT, NR>;
+template <int D, int B, int ROT>
+__global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, 1) attn_scored_kernel(ScoredArgs a) {
+  using C = CScored<D, B, ROT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) uint32_t s_lut[C::LUT * 32];
-  __shared__ RowInfo s_row[8 * NR];
+  __shared__ RowInfo s_row[8];
   __shared__ int8_t s_depth[64];
   __shared__ int s_abort;
 
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(CScored<D, B, ROT, NR>::THREADS, 1) attn_score
   int seqlen, n;
   scored_lengths(a, b, threadIdx.x == 0, seqlen, n);
   const int base = seqlen - n;
-  if (threadIdx.x < 8 * NR) s_row[threadIdx.x] = scored_row(a, b, kvh, rg * 8 + threadIdx.x, seqlen, n);
+  if (threadIdx.x < 8) s_row[threadIdx.x] = scored_row(a, b, kvh, rg * 8 + threadIdx.x, seqlen, n);
   if (warp >= 2) scored_depths(a, b, n, threadIdx.x - 64, s_depth);
   uint32_t qf[C::NB_W][4];
   if (warp < C::NCW) {
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(CScored<D, B, ROT, NR>::THREADS, 1) attn_score
   // n_split runs of tiles; the tiles inside [flo, fhi) are seen whole by every
   // row that sees anything.
   int glo = 0x7fffffff, ghi = 0, flo = 0, fhi = 0x7fffffff;
-  for (int r = 0; r < 8 * NR; ++r) {
+  for (int r = 0; r < 8; ++r) {
     const int lo = s_row[r].lo, hi = s_row[r].hi;
     if (lo < hi) {
       glo = min(glo, lo);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(CScored<D, B, ROT, NR>::THREADS, 1) attn_score
   float* qb_warp = reinterpret_cast<float*>(smem + C::OFF_QB) + warp * C::NB_W * 8;
   q_block_bias<C::NB_W>(qf, lane, qb_warp);
   const uint32_t qb = smem_u32(qb_warp) + t * 8;
-  const RowInfo mine = s_row[lane % (8 * NR)];  // the row whose masks this lane forms
+  const RowInfo mine = s_row[lane % (8)];  // the row whose masks this lane forms
   const int at0 = s_row[2 * t].at, at1 = s_row[2 * t + 1].at;
   const float sl0 = s_row[2 * t].slope, sl1 = s_row[2 * t + 1].slope;
   const bool tree = a.tree != nullptr, biased = a.slopes != nullptr;
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(CScored<D, B, ROT, NR>::THREADS, 1) attn_score
         pl[0] = movmatrix_trans(pack_half2(y0 - __low2float(h0), y1 - __high2float(h0)));
         pl[1] = movmatrix_trans(pack_half2(y2 - __low2float(h1), y3 - __high2float(h1)));
       }
-      pv_tile<D, B, ROT>(rb, lut_bytes, lane4, wh, lane, movmatrix_trans(X0), movmatrix_trans(X1), pl, acc, nA, nB);
+      pv_tile<D, B, ROT, C::PSPLIT>(rb, lut_bytes, lane4, wh, lane, movmatrix_trans(X0), movmatrix_trans(X1), pl, acc, nA, nB);
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[it % C::NSTAGE]);
@@ -285,37 +285,36 @@ __global__ void __launch_bounds__(CScored<D, B, ROT, NR>::THREADS, 1) attn_score
   decode_split_tail<D, C::RING, 256, true>(a, split, gid, b, kvh, rg, threadIdx.x, smem);
 }
 
-template <int D, int B, int ROT, int NR>
+template <int D, int B, int ROT>
 static cudaError_t launch_scored_d(const ScoredArgs& a, cudaStream_t stream) {
-  using C = CScored<D, B, ROT, NR>;
+  using C = CScored<D, B, ROT>;
   static bool configured[kMaxDevices] = {};  // the attribute is per function and device
   static ResidencyCache cap{};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= kMaxDevices || !configured[dev]) {
-    e = cudaFuncSetAttribute(attn_scored_kernel<D, B, ROT, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(attn_scored_kernel<D, B, ROT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) configured[dev] = true;
   }
-  return launch_split_decode(attn_scored_kernel<D, B, ROT, NR>, a, C::THREADS, C::SMEM, &cap, stream, NR);
+  return launch_split_decode(attn_scored_kernel<D, B, ROT>, a, C::THREADS, C::SMEM, &cap, stream);
 }
 
-template <int B>
+template <int D, int B, int ROT>
+static cudaError_t launch_scored_any(const ScoredArgs& a, cudaStream_t stream) {
+  return a.tiles ? launch_scored_tiles_d<D, B, ROT>(a, stream) : launch_scored_d<D, B, ROT>(a, stream);
+}
+
+template <int B, int ROT>
 static cudaError_t launch_scored_bits(const ScoredArgs& a, cudaStream_t stream) {
-  if (a.rot) {
-    switch (a.head_dim) {
-      case 128: return launch_scored_d<128, B, 1, 1>(a, stream);
-      case 256: return launch_scored_d<256, B, 1, 1>(a, stream);
-      case 512: return launch_scored_d<512, B, 1, 1>(a, stream);
-      default: return cudaErrorInvalidValue;
-    }
-  }
   switch (a.head_dim) {
-    case 64: return launch_scored_d<64, B, 0, 1>(a, stream);
-    case 128: return launch_scored_d<128, B, 0, 1>(a, stream);
-    case 256: return launch_scored_d<256, B, 0, 1>(a, stream);
-    case 512: return launch_scored_d<512, B, 0, 1>(a, stream);
+    case 64:
+      if constexpr (ROT) return cudaErrorInvalidValue;
+      else return launch_scored_any<64, B, 0>(a, stream);
+    case 128: return launch_scored_any<128, B, ROT>(a, stream);
+    case 256: return launch_scored_any<256, B, ROT>(a, stream);
+    case 512: return launch_scored_any<512, B, ROT>(a, stream);
     default: return cudaErrorInvalidValue;
   }
 }

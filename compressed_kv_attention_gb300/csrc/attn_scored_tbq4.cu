@@ -1,9 +1,11 @@
 // attn_scored_tbq4.cu — attn_scored and attn_tree over caches with 4 bits per V
-// code, both rotations; kernel in attn_scored_kernel.cuh.
+// code; kernels in attn_scored_kernel.cuh.
 #include "attn_scored_kernel.cuh"
 
 namespace ckv {
 
-cudaError_t launch_scored_mma4(const ScoredArgs& a, cudaStream_t stream) { return launch_scored_bits<4>(a, stream); }
+cudaError_t launch_scored_tbq4(const ScoredArgs& a, cudaStream_t stream) {
+  return launch_scored_bits<4, 0>(a, stream);
+}
 
 }  // namespace ckv

@@ -1,0 +1,786 @@
+// attn_scored_tiles.cuh — attn_scored and attn_tree with many query rows, on
+// tcgen05: one CTA owns 128 query rows of one kv head (128 / G tokens x G heads)
+// and walks its keys in steps of 64.
+//
+//   S = Q K_hat^T   M = 128, N = 64, K = D. K_hat = q d16 has up to 18
+//                   significant bits and enters as an exact fp16 pair hi + lo,
+//                   two products into one accumulator.
+//   O += P' C       P' = p * norm as fp16 (a pair hi + lo up to head dim 128
+//                   and for the rotated tiers), C the V centroids; M = 128,
+//                   K = 64.
+// Four roles overlap:
+//   warps 0-3   softmax: one row per thread, S from TMEM, cap, bias and mask in
+//               registers, P' to shared memory; the running maximum moves only
+//               when it grows by 2^2 or more (O in TMEM is rescaled then; P'
+//               stays below 4 norms, fp16 for any norm up to a quarter of its
+//               range)
+//   warps 4-11  widening: codes from global memory (fetched a chunk ahead) to
+//               fp16 operands in a ring of shared-memory slots, each 128 dims
+//               of the step's K (hi, then lo) or V
+//   warp 12     issues the MMAs as slots fill; a slot is free again when its
+//               MMAs have completed
+// S is double-buffered up to head dim 256, so that S of the next step runs
+// under the softmax of this one. At D = 512 the 512 TMEM columns hold S (64)
+// and 448 output dims; the last 64 dims of P' C go through S's columns once the
+// softmax has read them and are summed in the softmax threads' registers.
+// The 128-byte-swizzle K-major layout holds every operand.
+#pragma once
+
+#include "decode_common.cuh"
+#include "scored.cuh"
+
+namespace ckv {
+
+namespace {
+
+template <int D, int B, int ROT>
+struct CTiles {
+  static constexpr int M = 128, NKV = 64;
+  static constexpr int NB = D / 32;
+  static constexpr int NGRP = ROT ? D / kRotGroup : 1;
+  static constexpr int REC = record_bytes(D, B, NGRP);
+  static constexpr int CW = D < 128 ? D : 128;      // dims per slot
+  static constexpr int NCH = D / CW;                // slots per step of each operand
+  static constexpr int OT = D < 448 ? D : 448;      // output dims in TMEM
+  static constexpr int OR = D - OT;                 // output dims in registers
+  static constexpr int NS = D == 512 ? 1 : 2;       // S buffers
+  static constexpr int OCOL = 64 * NS;              // first O column
+  static constexpr bool PSPLIT = ROT || D <= 128;
+  static constexpr int LUT = B == 3 ? 64 : 16;
+  static constexpr int SLOT = NKV * CW * 2;
+  static constexpr int P_BYTES = M * NKV * 2;
+  static constexpr int Q_OFF = 0;
+  static constexpr int P_OFF = M * D * 2;
+  static constexpr int RING_OFF = P_OFF + (PSPLIT ? 2 : 1) * P_BYTES;
+  static constexpr int TAIL = LUT * 128 + 2 * NKV * 4 + M * 4 + M * static_cast<int>(sizeof(RowInfo));
+  static constexpr int BUDGET = 227 * 1024 - 1024 - 1024;  // alignment, static shared memory
+  static constexpr int NSLOT_FIT = (BUDGET - RING_OFF - TAIL) / SLOT;
+  static constexpr int NSLOT = NSLOT_FIT > 8 ? 8 : NSLOT_FIT;
+  static_assert(NSLOT >= 3, "a K chunk takes two slots");
+  static constexpr int LUT_OFF = RING_OFF + NSLOT * SLOT;
+  static constexpr int NORM_OFF = LUT_OFF + LUT * 128;
+  static constexpr int INV_OFF = NORM_OFF + 2 * NKV * 4;
+  static constexpr int ROW_OFF = INV_OFF + M * 4;
+  static constexpr int BYTES = ROW_OFF + M * static_cast<int>(sizeof(RowInfo));
+  // At least half the SM's shared memory: one CTA, and its 512 TMEM columns, per SM.
+  static constexpr int SMEM = (BYTES + 1024 > 120 * 1024 ? BYTES + 1024 : 120 * 1024);
+  static constexpr int THREADS = 512;
+  static constexpr int WIDEN = 256;                 // threads of the widening role
+  // Output staging of the epilogue: RP rows at a time, padded by 16 bytes.
+  static constexpr int STRIDE = D + 4;
+  static constexpr int RP = 64 * STRIDE * 4 <= LUT_OFF ? 64 : 32;
+  static_assert(RP * STRIDE * 4 <= LUT_OFF, "staging fits the operands' memory");
+};
+
+}  // namespace
+
+template <int D, int B, int ROT>
+__global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a) {
+  using C = CTiles<D, B, ROT>;
+  constexpr int M = C::M, NKV = C::NKV, CW = C::CW, NCH = C::NCH, NS = C::NS, NSLOT = C::NSLOT;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ uint32_t s_tmem;
+  __shared__ __align__(8) uint64_t b_full[8], b_free[8], b_sfull[2], b_sfree[2], b_pfull, b_pvdone, b_tail;
+  __shared__ int s_abort, s_red[4][4];
+  __shared__ int8_t s_depth[64];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* const sQ = smem + C::Q_OFF;
+  uint8_t* const sP = smem + C::P_OFF;
+  uint8_t* const ring = smem + C::RING_OFF;
+  uint32_t* const sLut = reinterpret_cast<uint32_t*>(smem + C::LUT_OFF);
+  float* const sNorm = reinterpret_cast<float*>(smem + C::NORM_OFF);
+  float* const sInv = reinterpret_cast<float*>(smem + C::INV_OFF);
+  RowInfo* const sRow = reinterpret_cast<RowInfo*>(smem + C::ROW_OFF);
+
+  const int G = a.n_q_heads / a.n_kv_heads;
+  const int QT = M / G;  // query tokens per tile (rows QT G .. 127 are padding)
+  const int n_qt = (a.n_q + QT - 1) / QT;
+  const int split = blockIdx.x % a.n_split;
+  const int tile = blockIdx.x / a.n_split;
+  const int qt = n_qt - 1 - tile % n_qt, bh = tile / n_qt;  // the later tokens of a prompt see more keys: first
+  const int b = bh / a.n_kv_heads, kvh = bh % a.n_kv_heads;
+  const int q0 = qt * QT;
+  const int rows = min(QT, a.n_q - q0) * G;  // real rows of the tile
+
+  if (warp == 0) tmem_alloc(&s_tmem, 512);
+  if (tid == 32) {
+    for (int s = 0; s < NSLOT; ++s) {
+      mbar_init(&b_full[s], C::WIDEN / 32);
+      mbar_init(&b_free[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&b_sfull[s], 1);
+      mbar_init(&b_sfree[s], 4);
+    }
+    mbar_init(&b_pfull, 4);
+    mbar_init(&b_pvdone, 1);
+    mbar_init(&b_tail, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  {
+    constexpr float inv = 1.0f / centroid_scale(B);
+    for (int e = tid; e < C::LUT * 32; e += C::THREADS) {
+      const int f = e >> 5;
+      const int klo = (B == 4) ? f : (f & ((1 << B) - 1));
+      const int khi = (B == 4) ? f : (f >> B);
+      sLut[e] = pack_half2(tbq_centroid<B>(klo) * inv, tbq_centroid<B>(khi) * inv);
+    }
+  }
+  griddep_wait();
+
+  // ---- rows, their common span [glo, ghi), and the part [flo, fhi) that every row sees ----
+  int seqlen, n;
+  scored_lengths(a, b, tid == 0, seqlen, n);
+  const int base = seqlen - n;
+  const bool tree = a.tree != nullptr;
+  if (tid >= 448) scored_depths(a, b, n, tid - 448, s_depth);
+  RowInfo row{0, 0, 0, 0.0f, 0ull};
+  if (tid < M) {
+    if (tid < rows) row = scored_row(a, b, kvh, q0 * G + tid, seqlen, n);
+    sRow[tid] = row;
+    const bool some = row.lo < row.hi;
+    const int lo0 = __reduce_min_sync(0xffffffffu, some ? row.lo : 0x7fffffff);
+    const int hi1 = __reduce_max_sync(0xffffffffu, some ? row.hi : 0);
+    const int lo1 = __reduce_max_sync(0xffffffffu, some ? row.lo : 0);
+    const int hi0 = __reduce_min_sync(0xffffffffu, some ? (tree ? min(base, row.hi) : row.hi) : 0x7fffffff);
+    if (lane == 0) s_red[warp][0] = lo0, s_red[warp][1] = hi1, s_red[warp][2] = lo1, s_red[warp][3] = hi0;
+  }
+  // ---- Q to shared memory: fp16 (bf16 is converted, exact within fp16's range) ----
+  for (int piece = tid; piece < M * (D / 8); piece += C::THREADS) {
+    const int r = piece / (D / 8), k0 = (piece % (D / 8)) * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (r < rows) {
+      const int64_t qrow = ((int64_t)b * a.n_q + q0 + r / G) * a.n_q_heads + kvh * G + r % G;
+      v = __ldg(reinterpret_cast<const uint4*>(a.q + qrow * D + k0));
+      if (a.q_bf16) {
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+          w[i] = pack_half2(__low2float(x), __high2float(x));
+        }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    *reinterpret_cast<uint4*>(sQ + sw128_offset(r, k0, M)) = v;
+  }
+  fence_proxy_async();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  int glo = 0x7fffffff, ghi = 0, flo = 0, fhi = 0x7fffffff;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    glo = min(glo, s_red[w][0]);
+    ghi = max(ghi, s_red[w][1]);
+    flo = max(flo, s_red[w][2]);
+    fhi = min(fhi, s_red[w][3]);
+  }
+  const int lo_s = ghi > glo ? glo / NKV : 0, hi_s = ghi > glo ? (ghi + NKV - 1) / NKV : 0;
+  const int s0 = lo_s + static_cast<int>((int64_t)split * (hi_s - lo_s) / a.n_split);
+  const int n_steps = lo_s + static_cast<int>((int64_t)(split + 1) * (hi_s - lo_s) / a.n_split) - s0;
+  const int64_t n_rec = a.capacity / kTile;
+  const uint8_t* const stream = a.cache + (int64_t)(b * a.n_kv_heads + kvh) * n_rec * C::REC;
+
+  // A wait that runs out raises the flag; every later wait is skipped, so that all roles finish.
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!*(volatile int*)&s_abort && !mbar_wait(bar, parity & 1u)) {
+      *(volatile int*)&s_abort = 1;
+      raise_flag(a.flag, kFlagWaitTimeout);
+    }
+  };
+
+  float m_used = -INFINITY, l_sum = 0.0f;
+  float otail[C::OR > 0 ? C::OR : 1];
+  const uint32_t row_tmem = tmem + ((uint32_t)(warp & 3) * 32u << 16);
+
+  if (warp < 4) {
+    // ------------------------------------------------------------- softmax --
+#pragma unroll
+    for (int i = 0; i < (C::OR > 0 ? C::OR : 1); ++i) otail[i] = 0.0f;
+    auto load_norm = [&](int step) {  // threads 0..63
+      const int64_t pos = (int64_t)(s0 + step) * NKV + tid;
+      return (!ROT && tid < NKV && step < n_steps && pos < seqlen)
+                 ? __half2float(*reinterpret_cast<const __half*>(stream + pos / kTile * C::REC + v_norm_offset(D, B) +
+                                                                 2 * (pos % kTile)))
+                 : 0.0f;
+    };
+    auto add_tail = [&](int step) {  // the last output dims of a step's P' C
+      if constexpr (C::OR > 0) {
+        wait(&b_tail, step);
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < C::OR; h += 32) {
+          uint32_t tv[32];
+          tmem_ld32(row_tmem + h, tv);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) otail[h + i] += __uint_as_float(tv[i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_sfree[0]);
+      }
+    };
+    float nrm = load_norm(0);
+    for (int i = 0; i < n_steps; ++i) {
+      const int buf = i % NS;
+      if constexpr (!ROT) {
+        if (tid < NKV) sNorm[(i & 1) * NKV + tid] = nrm;
+        named_bar(1, 128);
+        nrm = load_norm(i + 1);
+      }
+      if (i > 0) add_tail(i - 1);
+      wait(&b_sfull[buf], i / NS);
+      tc_fence_after();
+      // Logits of 32 columns at a time. At D = 512 the registers hold the tail
+      // dims, so the logits go back to S's columns until their exponentials.
+      constexpr bool KEEP = C::OR == 0;
+      float x[KEEP ? 2 : 1][32];
+      const int pos0 = (s0 + i) * NKV;
+      uint64_t see = row.hi > 0 ? ~0ull : 0ull;
+      if (pos0 < flo || pos0 + NKV > fhi) see = scored_step_bits(row, tree, base, pos0);
+      const bool masked = __any_sync(0xffffffffu, see != ~0ull);
+      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float (&v)[32] = x[KEEP ? h : 0];
+        uint32_t sv[32];
+        tmem_ld32(row_tmem + 64 * buf + 32 * h, sv);
+        tmem_ld_wait();
+        if (KEEP && h == 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b_sfree[buf]);
+        }
+        if (a.cap_log2 == 0.0f) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(sv[j]) * a.mul;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = a.cap_log2 * tanh_f32(__uint_as_float(sv[j]) * a.mul);
+        }
+        if (a.slopes) {
+          const int p0 = pos0 + 32 * h;
+          if (tree && p0 + 32 > base) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              v[j] = fmaf(-row.slope, static_cast<float>(abs(row.at - scored_key_at(s_depth, tree, base, p0 + j))), v[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(-row.slope, static_cast<float>(abs(row.at - p0 - j)), v[j]);
+          }
+        }
+        if (masked) {
+          const uint32_t bits = static_cast<uint32_t>(see >> (32 * h));
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = (bits >> j & 1u) ? v[j] : -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
+        if constexpr (!KEEP) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sv[j] = __float_as_uint(v[j]);
+          tmem_st32(row_tmem + 64 * buf + 32 * h, sv);
+        }
+      }
+      if constexpr (!KEEP) tmem_st_wait();
+      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+      // P' and (for a rescale) O are free once the step before has been multiplied.
+      if (i > 0) wait(&b_pvdone, i - 1);
+      tc_fence_after();
+      const bool need = mx > m_used + 2.0f;  // also when m_used is -inf and a key is seen
+      if (__any_sync(0xffffffffu, need)) {
+        const float f = need ? ((m_used == -INFINITY) ? 0.0f : fast_exp2(m_used - mx)) : 1.0f;
+        if (i > 0) {
+#pragma unroll 1
+          for (int c0 = C::OCOL; c0 < C::OCOL + C::OT; c0 += 32) {
+            uint32_t ov[32];
+            tmem_ld32(row_tmem + c0, ov);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
+            tmem_st32(row_tmem + c0, ov);
+          }
+          tmem_st_wait();
+        }
+#pragma unroll
+        for (int k = 0; k < C::OR; ++k) otail[k] *= f;
+        l_sum *= f;
+        if (need) m_used = mx;
+      }
+      const float mref = (m_used == -INFINITY) ? 0.0f : m_used;  // nothing seen yet: every x is -inf
+      float ps[2] = {0.0f, 0.0f};
+      const float4* n4 = reinterpret_cast<const float4*>(sNorm + (i & 1) * NKV);
+#pragma unroll
+      for (int c = 0; c < NKV / 8; ++c) {
+        float (&v)[32] = x[KEEP ? c / 4 : 0];
+        if constexpr (!KEEP) {
+          if (c % 4 == 0) {
+            uint32_t sv[32];
+            tmem_ld32(row_tmem + 64 * buf + 8 * c, sv);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(sv[j]);
+          }
+        }
+        float y[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int j = 8 * (c % 4) + 4 * h;
+          const float p0 = fast_exp2(v[j] - mref), p1 = fast_exp2(v[j + 1] - mref);
+          const float p2 = fast_exp2(v[j + 2] - mref), p3 = fast_exp2(v[j + 3] - mref);
+          ps[h] += (p0 + p1) + (p2 + p3);
+          if constexpr (ROT) {
+            y[4 * h] = p0, y[4 * h + 1] = p1, y[4 * h + 2] = p2, y[4 * h + 3] = p3;
+          } else {  // the norm of a key that the row does not see may hold any bytes
+            const float4 nn = n4[2 * c + h];
+            y[4 * h] = p0 > 0.0f ? p0 * nn.x : 0.0f;
+            y[4 * h + 1] = p1 > 0.0f ? p1 * nn.y : 0.0f;
+            y[4 * h + 2] = p2 > 0.0f ? p2 * nn.z : 0.0f;
+            y[4 * h + 3] = p3 > 0.0f ? p3 * nn.w : 0.0f;
+          }
+        }
+        uint32_t hi[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) hi[k] = pack_half2(y[2 * k], y[2 * k + 1]);
+        *reinterpret_cast<uint4*>(sP + sw128_offset(tid, 8 * c, M)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if constexpr (C::PSPLIT) {
+          uint32_t lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const __half2 hh = *reinterpret_cast<const __half2*>(&hi[k]);
+            lo[k] = pack_half2(y[2 * k] - __low2float(hh), y[2 * k + 1] - __high2float(hh));
+          }
+          *reinterpret_cast<uint4*>(sP + C::P_BYTES + sw128_offset(tid, 8 * c, M)) =
+              make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      l_sum += ps[0] + ps[1];
+      fence_proxy_async();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b_pfull);
+    }
+    if (n_steps > 0) {
+      add_tail(n_steps - 1);
+      wait(&b_pvdone, n_steps - 1);
+      tc_fence_after();
+    }
+    sInv[tid] = l_sum > 0.0f ? 1.0f / l_sum : 0.0f;
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ widening --
+    const int wt = tid - 128;  // 0 .. 255
+    int q = 0;                 // slots filled
+    auto slot_wait = [&](int k) {
+      if (k >= NSLOT) wait(&b_free[k % NSLOT], k / NSLOT - 1);
+    };
+    auto slot_done = [&](int k) {
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b_full[k % NSLOT]);
+    };
+    // K chunk c of a step: 4 records x CW / 32 blocks x 32 lanes of 16 bytes,
+    // each 8 dims of tokens kpp and kpp + 8 of a record.
+    constexpr int PIECES = 4 * (CW / 32) * 32, KR = PIECES / C::WIDEN;
+    static_assert(KR >= 1 && PIECES % C::WIDEN == 0, "K pieces per thread");
+    const int kq = lane >> 3, kpp = lane & 7;
+    uint4 kw[KR];
+    uint32_t ks[KR];  // the two tokens' scales
+    auto fetch_k = [&](int step, int c) {
+      if (step >= n_steps) return;
+#pragma unroll
+      for (int r = 0; r < KR; ++r) {
+        const int u = r * 8 + (wt >> 5);  // (record, block) of this warp
+        const int64_t rec = (int64_t)(s0 + step) * 4 + u / (CW / 32);
+        const int blk = c * (CW / 32) + u % (CW / 32);
+        if (rec < n_rec) {
+          const uint8_t* p = stream + rec * C::REC;
+          kw[r] = *reinterpret_cast<const uint4*>(p + (blk * 32 + 4 * kpp + kq) * 16);
+          const uint16_t* sc = reinterpret_cast<const uint16_t*>(p + k_scale_offset(D)) + blk;
+          ks[r] = sc[kpp * C::NB] | (uint32_t)sc[(kpp + 8) * C::NB] << 16;
+        } else {
+          kw[r] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+          ks[r] = 0u;
+        }
+      }
+    };
+    auto widen_k = [&](int step, int c) {
+      uint4 w4[KR];
+      uint32_t sc[KR];
+#pragma unroll
+      for (int r = 0; r < KR; ++r) w4[r] = kw[r], sc[r] = ks[r];
+      if (c + 1 < NCH) fetch_k(step, c + 1);
+      else fetch_k(step + 1, 0);
+      slot_wait(q);
+      slot_wait(q + 1);
+      uint8_t* const s_hi = ring + (q % NSLOT) * C::SLOT;
+      uint8_t* const s_lo = ring + ((q + 1) % NSLOT) * C::SLOT;
+#pragma unroll
+      for (int r = 0; r < KR; ++r) {
+        const int u = r * 8 + (wt >> 5);
+        const int row0 = u / (CW / 32) * kTile + kpp, k0 = (u % (CW / 32)) * 32 + 8 * kq;
+        const uint32_t w[4] = {w4[r].x, w4[r].y, w4[r].z, w4[r].w};
+#pragma unroll
+        for (int hs = 0; hs < 2; ++hs) {
+          const uint32_t d1 = hs ? sc[r] >> 16 : sc[r] & 0xffffu;
+          const uint32_t dd = d1 | d1 << 16;
+          const __half2 d2 = *reinterpret_cast<const __half2*>(&dd);
+          uint32_t qh[4], hi[4], lo[4];
+          i8x4_to_half2x2(w[2 * hs], qh[0], qh[1]);
+          i8x4_to_half2x2(w[2 * hs + 1], qh[2], qh[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half2 qv = *reinterpret_cast<const __half2*>(&qh[e]);
+            const __half2 h = __hmul2(qv, d2);
+            const __half2 l = __hfma2(qv, d2, __hneg2(h));
+            hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+            lo[e] = *reinterpret_cast<const uint32_t*>(&l);
+          }
+          const uint32_t off = sw128_offset(row0 + 8 * hs, k0, NKV);
+          *reinterpret_cast<uint4*>(s_hi + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(s_lo + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      slot_done(q);
+      slot_done(q + 1);
+      q += 2;
+    };
+    // V chunk c of a step: units of (lane stream, 8 dims), 16 fields of 2B
+    // bits in B words of the stream. Unit v = 16 (...) + 4 record + (stream % 4).
+    constexpr int GDIM = D / 8;                             // dims per lane stream
+    constexpr int SUB = GDIM / 8 > 0 ? GDIM / 8 : 1;        // 8-dim parts of a stream
+    constexpr int UNITS = 16 * (CW / 8), VR = (UNITS + C::WIDEN - 1) / C::WIDEN;
+    static_assert(VR == 1, "one V unit per thread and chunk");
+    const bool v_on = wt < UNITS;
+    const int v_rec = (wt >> 2) & 3, v_t = wt & 3, v_part = wt >> 4;  // 8-dim part of the chunk
+    constexpr int GR = v_granule(D, B);
+    uint32_t vw[B], vn[2] = {0u, 0u};
+    auto v_chunk = [&](int k) { return C::OR > 0 ? (k + NCH - 1) % NCH : k; };  // D = 512: the tail's chunk first
+    auto fetch_v = [&](int step, int k) {
+      if (step >= n_steps || !v_on) return;
+      const int part = v_chunk(k) * (CW / 8) + v_part;  // dims 8 part .. 8 part + 7
+      const int L = 4 * (part / SUB) + v_t, w0 = (part % SUB) * B;
+      const int64_t rec = (int64_t)(s0 + step) * 4 + v_rec;
+      const uint8_t* p = stream + rec * C::REC;
+#pragma unroll
+      for (int w = 0; w < B; ++w) {
+        const int sb = 4 * (w0 + w);
+        vw[w] = rec < n_rec ? *reinterpret_cast<const uint32_t*>(p + v_code_offset(D) + ((sb / GR) * 32 + L) * GR + sb % GR)
+                            : 0u;
+      }
+      if constexpr (ROT) {  // the norms of positions 2t, 2t + 1 and 2t + 8, 2t + 9
+        const uint8_t* nb = p + v_norm_offset(D, B) + 2 * (kTile * (8 * part / kRotGroup) + 2 * v_t);
+        vn[0] = rec < n_rec ? *reinterpret_cast<const uint32_t*>(nb) : 0u;
+        vn[1] = rec < n_rec ? *reinterpret_cast<const uint32_t*>(nb + 16) : 0u;
+      }
+    };
+    auto widen_v = [&](int step, int k) {
+      uint32_t w[B], nn[2] = {vn[0], vn[1]};
+#pragma unroll
+      for (int e = 0; e < B; ++e) w[e] = vw[e];
+      if (k + 1 < NCH) fetch_v(step, k + 1);
+      else fetch_v(step + 1, 0);
+      if constexpr (ROT) {
+        const int pos0 = (s0 + step) * NKV;
+        if (pos0 < flo || pos0 + NKV > fhi) {  // norms of positions that no row sees may hold any bytes
+          uint32_t any = 0u;
+          for (int rec = 0; rec < 4; ++rec) {
+            uint32_t m = 0u;
+            for (int r = lane; r < M; r += 32) m |= scored_tile_bits(sRow[r], tree, base, pos0 + rec * kTile);
+            m = __reduce_or_sync(0xffffffffu, m);
+            if (rec == v_rec) any = m;
+          }
+          const uint32_t ma = any >> (2 * v_t), mb = any >> (2 * v_t + 8);
+          nn[0] &= (ma & 1u ? 0xffffu : 0u) | (ma & 2u ? 0xffff0000u : 0u);
+          nn[1] &= (mb & 1u ? 0xffffu : 0u) | (mb & 2u ? 0xffff0000u : 0u);
+        }
+      }
+      slot_wait(q);
+      uint8_t* const dst = ring + (q % NSLOT) * C::SLOT;
+      if (v_on) {
+        const uint32_t lut = smem_u32(sLut) + (uint32_t)(lane << 2);
+        const int tok = v_rec * kTile + 2 * v_t;
+        auto field = [&](int f) {  // dim 2 (f / 4) + (f & 1), positions + 8 (f >> 1 & 1)
+          uint32_t val;
+          if constexpr (B == 3) {
+            const int bit = 6 * f, wi = bit >> 5, sh = bit & 31;
+            uint32_t y = w[wi] >> sh;
+            if (sh > 26 && wi + 1 < B) y |= w[wi + 1 < B ? wi + 1 : wi] << (32 - sh);
+            val = lds32(lut + ((y & 63u) << 7));
+          } else if constexpr (B == 2) {
+            val = lds32(lut + (((w[f >> 3] >> (4 * (f & 7))) & 15u) << 7));
+          } else {
+            const uint32_t y = (w[f >> 2] >> (8 * (f & 3))) & 255u;
+            val = __byte_perm(lds32(lut + ((y & 15u) << 7)), lds32(lut + ((y >> 4) << 7)), 0x7610);
+          }
+          if constexpr (ROT) val = hmul2_u32(val, nn[f >> 1 & 1]);
+          return val;
+        };
+        // A warp holds two parts, whose rows share their banks: one writes the
+        // upper eight positions of a record while the other writes the lower.
+        const bool flip = v_part & 1;
+#pragma unroll
+        for (int f = 0; f < 16; ++f) {
+          if (f & 2) continue;
+          const uint32_t lo = field(f), hi = field(f | 2);
+          const int dim = v_part * 8 + 2 * (f >> 2) + (f & 1);
+          *reinterpret_cast<uint32_t*>(dst + sw128_offset(dim, tok + (flip ? 8 : 0), CW)) = flip ? hi : lo;
+          *reinterpret_cast<uint32_t*>(dst + sw128_offset(dim, tok + (flip ? 0 : 8), CW)) = flip ? lo : hi;
+        }
+      }
+      slot_done(q);
+      ++q;
+    };
+    fetch_k(0, 0);
+    fetch_v(0, 0);
+    auto all_k = [&](int step) {
+      for (int c = 0; c < NCH; ++c) widen_k(step, c);
+    };
+    if (NS == 2 && n_steps > 0) all_k(0);
+    for (int i = 0; i < n_steps; ++i) {
+      if constexpr (NS == 1) all_k(i);
+      else if (i + 1 < n_steps) all_k(i + 1);
+      for (int k = 0; k < NCH; ++k) widen_v(i, k);
+    }
+  } else {
+    if (warp == 12 && lane == 0) {
+      // --------------------------------------------------------------- MMA --
+      const uint32_t q_base = smem_u32(sQ), p_base = smem_u32(sP), r_base = smem_u32(ring);
+      int q = 0;
+      auto s_step = [&](int i) {
+        const int buf = i % NS;
+        if (i >= NS) wait(&b_sfree[buf], i / NS - 1);
+        for (int c = 0; c < 2 * NCH; ++c) {  // chunk c / 2, hi then lo
+          wait(&b_full[q % NSLOT], q / NSLOT);
+          tc_fence_after();
+          const uint32_t slot = r_base + (q % NSLOT) * C::SLOT;
+#pragma unroll
+          for (int ks = 0; ks < CW / 16; ++ks) {
+            const int kd = (c >> 1) * (CW / 16) + ks;
+            umma_f16(tmem + 64 * buf, umma_desc_sw128(q_base + (kd >> 2) * (M * 128) + (kd & 3) * 32),
+                     umma_desc_sw128(slot + (ks >> 2) * (NKV * 128) + (ks & 3) * 32), umma_idesc_f16_f32(M, NKV),
+                     c > 0 || ks > 0);
+          }
+          umma_commit(&b_free[q % NSLOT]);
+          ++q;
+        }
+        umma_commit(&b_sfull[buf]);
+      };
+      // O columns [col, col + N) += P' C over the step's 64 tokens, C rows from `dims`.
+      auto pv = [&](uint32_t col, uint32_t dims, uint32_t idesc, bool keep) {
+#pragma unroll
+        for (int ks = 0; ks < NKV / 16; ++ks) {
+          const uint64_t bd = umma_desc_sw128(dims + ks * 32);
+          umma_f16(tmem + col, umma_desc_sw128(p_base + ks * 32), bd, idesc, keep || ks > 0);
+          if constexpr (C::PSPLIT) umma_f16(tmem + col, umma_desc_sw128(p_base + C::P_BYTES + ks * 32), bd, idesc, true);
+        }
+      };
+      auto pv_step = [&](int i) {
+        wait(&b_pfull, i);
+        tc_fence_after();
+        for (int k = 0; k < NCH; ++k) {
+          wait(&b_full[q % NSLOT], q / NSLOT);
+          tc_fence_after();
+          const uint32_t slot = r_base + (q % NSLOT) * C::SLOT;
+          if constexpr (C::OR > 0) {
+            if (k == 0) {  // the last chunk: its upper half to S's columns, its lower half to O
+              pv(0, slot + C::OR * 128, umma_idesc_f16_f32(M, C::OR), false);
+              umma_commit(&b_tail);
+              pv(C::OCOL + D - CW, slot, umma_idesc_f16_f32(M, CW - C::OR), i > 0);
+            } else {
+              pv(C::OCOL + (k - 1) * CW, slot, umma_idesc_f16_f32(M, CW), i > 0);
+            }
+          } else {
+            pv(C::OCOL + k * CW, slot, umma_idesc_f16_f32(M, CW), i > 0);
+          }
+          umma_commit(&b_free[q % NSLOT]);
+          ++q;
+        }
+        umma_commit(&b_pvdone);
+      };
+      if (NS == 2 && n_steps > 0) s_step(0);
+      for (int i = 0; i < n_steps; ++i) {
+        if constexpr (NS == 1) s_step(i);
+        else if (i + 1 < n_steps) s_step(i + 1);
+        pv_step(i);
+      }
+    }
+    __syncwarp();
+  }
+
+  // ---------------------------------------------------------------- epilogue --
+  // Rows leave TMEM one per thread; they cross to one row per warp through the
+  // operands' shared memory, C::RP rows at a time, there get the inverse
+  // transform (one split) and go out in whole lines.
+  const bool direct = a.n_split == 1;
+  float* const slot = a.part + (int64_t)blockIdx.x * (M * (D + 1));
+  float* const stage = reinterpret_cast<float*>(smem);
+  if (warp < 4 && tid < rows) {
+    const float lse = l_sum > 0.0f ? (m_used + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+    if (direct) a.lse[((int64_t)b * a.n_q + q0 + tid / G) * a.n_q_heads + kvh * G + tid % G] = lse;
+    else slot[(int64_t)M * D + tid] = lse;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  for (int r0 = 0; r0 < rows; r0 += C::RP) {
+    if (warp < 4 && warp * 32 >= r0 && warp * 32 < r0 + C::RP) {
+      const float inv = sInv[tid];
+      float* const dst = stage + (tid - r0) * C::STRIDE;
+#pragma unroll 1
+      for (int c = 0; c < C::OT; c += 32) {
+        uint32_t ov[32];
+        if (n_steps > 0) {
+          tmem_ld32(row_tmem + C::OCOL + c, ov);
+          tmem_ld_wait();
+        }
+#pragma unroll
+        for (int k = 0; k < 32; k += 4)
+          *reinterpret_cast<float4*>(dst + c + k) =
+              inv > 0.0f ? make_float4(__uint_as_float(ov[k]) * inv, __uint_as_float(ov[k + 1]) * inv,
+                                       __uint_as_float(ov[k + 2]) * inv, __uint_as_float(ov[k + 3]) * inv)
+                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      if constexpr (C::OR > 0) {
+#pragma unroll
+        for (int k = 0; k < C::OR; k += 4)
+          *reinterpret_cast<float4*>(dst + C::OT + k) =
+              inv > 0.0f ? make_float4(otail[k] * inv, otail[k + 1] * inv, otail[k + 2] * inv, otail[k + 3] * inv)
+                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+    }
+    __syncthreads();
+    for (int r = r0 + warp; r < min(rows, r0 + C::RP); r += C::THREADS / 32) {
+      float2 v[D / 64];
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e)
+        v[e] = *reinterpret_cast<const float2*>(stage + (r - r0) * C::STRIDE + 64 * e + 2 * lane);
+      if (direct) {
+        const int64_t orow = ((int64_t)b * a.n_q + q0 + r / G) * a.n_q_heads + kvh * G + r % G;
+        float* const o = a.out_type == kOutF32 ? a.out + orow * D
+                                               : reinterpret_cast<float*>(reinterpret_cast<uint16_t*>(a.out) + orow * D);
+        derotate_store_row<D, ROT, true>(v, lane, a.signs, o, centroid_scale(B), a.signs2, a.out_type);
+      } else {
+        derotate_store_row<D>(v, lane, nullptr, slot + (int64_t)r * D);
+      }
+    }
+    __syncthreads();
+  }
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// The n_split partials of every output row, merged exactly (log-sum-exp), and
+// the inverse transform: one CTA of 128 threads per row, the row's slots read
+// 16 bytes per thread with several in flight.
+template <int D, int B, int ROT>
+__global__ void __launch_bounds__(128) scored_merge_rows_kernel(ScoredArgs a) {
+  constexpr int M = 128, UNITS = D / 4, SG = 128 / UNITS > 0 ? 128 / UNITS : 1, PER = 8;
+  constexpr int64_t SLOT = M * (int64_t)(D + 1);
+  __shared__ float s_w[kMaxSplits];
+  __shared__ float s_red[4];
+  __shared__ __align__(16) float4 s_acc[SG][UNITS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_wait();
+  const int G = a.n_q_heads / a.n_kv_heads, QT = M / G, n_qt = (a.n_q + QT - 1) / QT;
+  const int64_t r = blockIdx.x;
+  const int h = static_cast<int>(r % a.n_q_heads);
+  const int64_t bq = r / a.n_q_heads;
+  const int qi = static_cast<int>(bq % a.n_q), b = static_cast<int>(bq / a.n_q);
+  const int64_t tile = ((int64_t)b * a.n_kv_heads + h / G) * n_qt + (n_qt - 1 - qi / QT);
+  const int rin = (qi % QT) * G + h % G;
+  const float* const base = a.part + tile * a.n_split * SLOT;
+  float m = -INFINITY;
+  for (int s = tid; s < a.n_split; s += 128) {
+    const float l = __ldcg(base + s * SLOT + (int64_t)M * D + rin);
+    s_w[s] = l;
+    m = fmaxf(m, l);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) s_red[warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  float total = 0.0f;
+  for (int s = 0; s < a.n_split; ++s) total += (s_w[s] == -INFINITY) ? 0.0f : exp2f((s_w[s] - m) * 1.4426950408889634f);
+  const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+  const int u = tid % UNITS, g = tid / UNITS;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (g < SG) {
+    for (int s0 = g; s0 < a.n_split; s0 += SG * PER) {
+      float4 x[PER];
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int s = s0 + j * SG;
+        if (s < a.n_split) x[j] = __ldcg(reinterpret_cast<const float4*>(base + s * SLOT + (int64_t)rin * D) + u);
+      }
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int s = s0 + j * SG;
+        if (s < a.n_split) {
+          const float w = (s_w[s] == -INFINITY) ? 0.0f : exp2f((s_w[s] - m) * 1.4426950408889634f) * inv;
+          acc.x = fmaf(w, x[j].x, acc.x);
+          acc.y = fmaf(w, x[j].y, acc.y);
+          acc.z = fmaf(w, x[j].z, acc.z);
+          acc.w = fmaf(w, x[j].w, acc.w);
+        }
+      }
+    }
+    s_acc[g][u] = acc;
+  }
+  __syncthreads();
+  if (warp) return;
+  const float* flat = reinterpret_cast<const float*>(s_acc);
+  float2 v[D / 64];
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) {
+    v[e] = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < SG; ++k) {
+      const float2 y = *reinterpret_cast<const float2*>(flat + k * D + 64 * e + 2 * lane);
+      v[e].x += y.x;
+      v[e].y += y.y;
+    }
+  }
+  float* const o = a.out_type == kOutF32 ? a.out + r * D
+                                         : reinterpret_cast<float*>(reinterpret_cast<uint16_t*>(a.out) + r * D);
+  derotate_store_row<D, ROT, true>(v, lane, a.signs, o, centroid_scale(B), a.signs2, a.out_type);
+  if (lane == 0) a.lse[r] = total > 0.0f ? m + logf(total) : -INFINITY;
+}
+
+template <int D, int B, int ROT>
+static cudaError_t launch_scored_tiles_d(const ScoredArgs& a, cudaStream_t stream) {
+  using C = CTiles<D, B, ROT>;
+  static bool configured[kMaxDevices] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices || !configured[dev]) {
+    e = cudaFuncSetAttribute(attn_scored_tiles_kernel<D, B, ROT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) configured[dev] = true;
+  }
+  const int QT = C::M / (a.n_q_heads / a.n_kv_heads), n_qt = (a.n_q + QT - 1) / QT;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((int64_t)a.batch * a.n_kv_heads * n_qt * a.n_split));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attn_scored_tiles_kernel<D, B, ROT>, a);
+  if (e != cudaSuccess || a.n_split == 1) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>((int64_t)a.batch * a.n_q * a.n_q_heads));
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, scored_merge_rows_kernel<D, B, ROT>, a);
+}
+
+}  // namespace ckv

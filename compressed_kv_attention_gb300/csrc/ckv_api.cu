@@ -913,22 +913,52 @@ ckv_status ckv_read_device_flag(const void* workspace, int32_t* flag, void* stre
 
 // ------------------------------------------- attn_scored, attn_tree, tree_accept --
 
-// Splits of an attn_scored / attn_tree call: the sequence's keys are those
-// that a row can see, which a window bounds on the host.
+// The form of an attn_scored / attn_tree call: 128-row tiles on tcgen05 where a
+// kv head has more than kTileRows query rows, else 8-row groups on mma.sync.
+constexpr int kTileRows = 32;
+struct ScoredPlan {
+  int tiles, n_row_groups, n_split;
+  size_t part, ws;  // offset of the partials, bytes of the workspace
+  int64_t groups;
+};
+
+// keys: how many of a sequence's keys its rows can see (a window bounds them on the host).
 static ckv_status plan_scored(const ckv_cache* cache, int64_t max_seq_len, int n_q, int n_q_heads, int64_t keys,
-                              int n_split, DecodePlan* p) {
-  ckv_status s = plan_decode(cache->head_dim, cache->n_kv_heads, cache->batch, max_seq_len, n_q, n_q_heads, n_split, p);
+                              int n_split, ScoredPlan* sp) {
+  DecodePlan p;
+  ckv_status s = plan_decode(cache->head_dim, cache->n_kv_heads, cache->batch, max_seq_len, n_q, n_q_heads, n_split, &p);
   if (s != CKV_OK) return s;
-  if (static_cast<int64_t>(cache->batch) * cache->n_kv_heads > 65535)
-    return fail(CKV_ERR_UNSUPPORTED, "batch * n_kv_heads above 65535");
-  if (!n_split) p->n_split = auto_split(p->groups, keys, cache->head_dim == 512 ? 4 : 8);
-  p->ws = p->n_split == 1 ? ws_header_bytes(p->groups, 1) : decode_ws_bytes(cache->head_dim, p->groups, p->n_split);
+  const int64_t bh = static_cast<int64_t>(cache->batch) * cache->n_kv_heads;
+  if (bh > 65535) return fail(CKV_ERR_UNSUPPORTED, "batch * n_kv_heads above 65535");
+  const int G = n_q_heads / cache->n_kv_heads;
+  const size_t row = sizeof(float);
+  sp->tiles = static_cast<int64_t>(G) * n_q > kTileRows && G <= 128;
+  sp->n_row_groups = p.n_row_groups;
+  sp->groups = p.groups;
+  if (sp->tiles) {
+    const int64_t units = bh * ((n_q + 128 / G - 1) / (128 / G)), steps = (keys + 63) / 64;
+    int64_t ns = n_split;
+    if (!ns) {
+      ns = num_sms() / units;
+      if (ns > steps) ns = steps;
+      if (ns > ckv::kMaxSplits) ns = ckv::kMaxSplits;
+      if (ns < 1) ns = 1;
+    }
+    if (units * ns > 0x7fffffffLL) return fail(CKV_ERR_UNSUPPORTED, "too many query tiles and splits");
+    sp->n_split = static_cast<int>(ns);
+    sp->part = 256;
+    sp->ws = 256 + (ns == 1 ? 0 : static_cast<size_t>(units) * ns * 128 * (cache->head_dim + 1) * row);
+    return CKV_OK;
+  }
+  sp->n_split = n_split ? n_split : auto_split(p.groups, keys, cache->head_dim == 512 ? 4 : 8);
+  sp->part = ws_header_bytes(p.groups, sp->n_split);
+  sp->ws = sp->n_split == 1 ? sp->part : decode_ws_bytes(cache->head_dim, p.groups, sp->n_split);
   return CKV_OK;
 }
 
 size_t ckv_attn_scored_workspace(const ckv_cache* cache, int64_t max_seq_len, int32_t n_q, int32_t n_q_heads,
                                  int32_t n_split) {
-  DecodePlan p;
+  ScoredPlan p;
   if (check_cache(cache) != CKV_OK ||
       plan_scored(cache, max_seq_len, n_q, n_q_heads, max_seq_len, n_split, &p) != CKV_OK)
     return 0;
@@ -952,7 +982,7 @@ static ckv_status run_scored(const ckv_cache* cache, const int32_t* seq_len, int
   if (max_seq_len > 0x7fffffffLL - 64) return fail(CKV_ERR_UNSUPPORTED, "max_seq_len above 2^31 - 65");
   int64_t keys = max_seq_len;
   if (score->window && !score->prefix_len && keys > (int64_t)score->window + n_q) keys = (int64_t)score->window + n_q;
-  DecodePlan p;
+  ScoredPlan p;
   s = plan_scored(cache, max_seq_len, n_q, n_q_heads, keys, n_split, &p);
   if (s != CKV_OK) return s;
   if (!seq_len || !q || !out || !lse) return fail(CKV_ERR_INVALID_ARG, "null seq_len/q/out/lse");
@@ -983,7 +1013,8 @@ static ckv_status run_scored(const ckv_cache* cache, const int32_t* seq_len, int
   a.n_q_heads = n_q_heads;
   a.n_split = p.n_split;
   a.n_row_groups = p.n_row_groups;
-  a.part = reinterpret_cast<float*>(base + ws_header_bytes(p.groups, p.n_split));
+  a.tiles = p.tiles;
+  a.part = reinterpret_cast<float*>(base + p.part);
   a.sub = a.part + static_cast<size_t>(p.groups) * p.n_split * ckv::merge_slot_floats(cache->head_dim);
   a.merge_ls = tr.ls;
   a.merge_nl = tr.nl;
@@ -1000,14 +1031,14 @@ static ckv_status run_scored(const ckv_cache* cache, const int32_t* seq_len, int
   a.prefix_len = score->prefix_len;
   a.doc_start = score->doc_start;
   a.window = score->window;
-  // The products carry 2^-24 (the codes enter the tensor cores as subnormals).
-  constexpr float kLog2e = 1.4426950408889634f, kCodes = 16777216.0f;
+  // The row groups' products carry 2^-24 (their codes enter the tensor cores as subnormals).
+  const float kLog2e = 1.4426950408889634f, kCodes = a.tiles ? 1.0f : 16777216.0f;
   a.cap_log2 = score->softcap * kLog2e;
   a.mul = score->softcap > 0.0f ? scale * kCodes / score->softcap : scale * kCodes * kLog2e;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a.v_bits == 2   ? ckv::launch_scored_mma2(a, st)
-                        : a.v_bits == 4 ? ckv::launch_scored_mma4(a, st)
-                                        : ckv::launch_scored_mma3(a, st);
+  const cudaError_t e = a.v_bits == 2   ? (a.rot ? ckv::launch_scored_rot2(a, st) : ckv::launch_scored_tbq2(a, st))
+                        : a.v_bits == 4 ? (a.rot ? ckv::launch_scored_rot4(a, st) : ckv::launch_scored_tbq4(a, st))
+                                        : (a.rot ? ckv::launch_scored_rot3(a, st) : ckv::launch_scored_tbq3(a, st));
   if (e != cudaSuccess) return cuda_fail(e, "scored attention launch");
   return CKV_OK;
 }

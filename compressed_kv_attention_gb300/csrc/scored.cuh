@@ -23,6 +23,10 @@ struct ScoredArgs : DecodeArgs {
   const int32_t* prefix_len; // [batch] or nullptr
   const int32_t* doc_start;  // [batch][n_q] or nullptr
   int window;                // 0: none
+  // The tcgen05 form (128 query rows per CTA): n_split shares of each tile's
+  // keys, partial rows at part ([tile][split][128][D + 1]: normalised rotated
+  // rows, then their lse) when there are several.
+  int tiles;
   // Without a cap (cap_log2 0) the logit is mul * S; with one it is
   // cap_log2 * tanh(mul * S).
   float mul, cap_log2;
@@ -110,6 +114,24 @@ __device__ __forceinline__ uint32_t scored_tile_bits(const RowInfo& r, bool tree
   return m;
 }
 
+// The same for the 64 positions from tpos on.
+__device__ __forceinline__ uint64_t scored_step_bits(const RowInfo& r, bool tree, int base, int64_t tpos) {
+  const int64_t l = r.lo - tpos, h = r.hi - tpos;
+  if (h <= 0 || l >= 64) return 0ull;
+  uint64_t m = h >= 64 ? ~0ull : (1ull << h) - 1ull;
+  if (l > 0) m &= ~((1ull << l) - 1ull);
+  if (tree) {
+    const int64_t off = tpos - base;
+    if (off >= 0) {
+      m &= off < 64 ? r.tree >> off : 0ull;
+    } else if (off > -64) {
+      const int before = static_cast<int>(-off);
+      m &= (r.tree << before) | ((1ull << before) - 1ull);
+    }
+  }
+  return m;
+}
+
 // tanh to about 4 units in the last place: x (1 - x^2/3 + 2 x^4/15 -
 // 17 x^6/315), its Taylor series, below 1/4 (the next term is 3e-7 of the
 // value there), else 1 - 2 / (1 + e^(2|x|)); the hardware's approximate tanh
@@ -137,8 +159,12 @@ __device__ __forceinline__ void scored_depths(const ScoredArgs& a, int b, int n,
     depth[tid] = tid < n ? static_cast<int8_t>(__popcll(a.tree[(int64_t)b * a.n_q + tid] & low_bits(n)) - 1) : 0;
 }
 
-cudaError_t launch_scored_mma2(const ScoredArgs& a, cudaStream_t stream);  // one translation unit per tier:
-cudaError_t launch_scored_mma3(const ScoredArgs& a, cudaStream_t stream);  // bits per V code, both rotations
-cudaError_t launch_scored_mma4(const ScoredArgs& a, cudaStream_t stream);
+// One translation unit per tier (bits per V code) and rotation.
+cudaError_t launch_scored_tbq2(const ScoredArgs& a, cudaStream_t stream);
+cudaError_t launch_scored_tbq3(const ScoredArgs& a, cudaStream_t stream);
+cudaError_t launch_scored_tbq4(const ScoredArgs& a, cudaStream_t stream);
+cudaError_t launch_scored_rot2(const ScoredArgs& a, cudaStream_t stream);
+cudaError_t launch_scored_rot3(const ScoredArgs& a, cudaStream_t stream);
+cudaError_t launch_scored_rot4(const ScoredArgs& a, cudaStream_t stream);
 
 }  // namespace ckv
