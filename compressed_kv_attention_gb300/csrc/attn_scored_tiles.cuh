@@ -9,15 +9,15 @@
 //                   and for the rotated tiers), C the V centroids; M = 128,
 //                   K = 64.
 // Four roles overlap:
-//   warps 0-3   softmax: one row per thread, S from TMEM, cap, bias and mask in
-//               registers, P' to shared memory; the running maximum moves only
-//               when it grows by 2^2 or more (O in TMEM is rescaled then; P'
-//               stays below 4 norms, fp16 for any norm up to a quarter of its
-//               range)
-//   warps 4-11  widening: codes from global memory (fetched a chunk ahead) to
-//               fp16 operands in a ring of shared-memory slots, each 128 dims
-//               of the step's K (hi, then lo) or V
-//   warp 12     issues the MMAs as slots fill; a slot is free again when its
+//   warps 0-7   softmax: two threads per row, 32 columns of S each, from TMEM;
+//               cap, bias and mask in registers, P' to shared memory; the
+//               running maximum moves only when it grows by 2^2 or more (O in
+//               TMEM is rescaled then; P' stays below 4 norms, fp16 for any
+//               norm up to a quarter of its range)
+//   warps 8-15  widening: codes from global memory (fetched two chunks ahead)
+//               to fp16 operands in a ring of shared-memory slots, each 128
+//               dims of the step's K (hi, then lo) or V
+//   warp 16     issues the MMAs as slots fill; a slot is free again when its
 //               MMAs have completed
 // S is double-buffered up to head dim 256, so that S of the next step runs
 // under the softmax of this one. At D = 512 the 512 TMEM columns hold S (64)
@@ -52,20 +52,23 @@ struct CTiles {
   static constexpr int Q_OFF = 0;
   static constexpr int P_OFF = M * D * 2;
   static constexpr int RING_OFF = P_OFF + (PSPLIT ? 2 : 1) * P_BYTES;
-  static constexpr int TAIL = LUT * 128 + 2 * NKV * 4 + M * 4 + M * static_cast<int>(sizeof(RowInfo));
+  static constexpr int TAIL = LUT * 128 + 2 * NKV * 4 + 4 * M * 4 + M * static_cast<int>(sizeof(RowInfo));
   static constexpr int BUDGET = 227 * 1024 - 1024 - 1024;  // alignment, static shared memory
   static constexpr int NSLOT_FIT = (BUDGET - RING_OFF - TAIL) / SLOT;
   static constexpr int NSLOT = NSLOT_FIT > 8 ? 8 : NSLOT_FIT;
   static_assert(NSLOT >= 3, "a K chunk takes two slots");
   static constexpr int LUT_OFF = RING_OFF + NSLOT * SLOT;
   static constexpr int NORM_OFF = LUT_OFF + LUT * 128;
-  static constexpr int INV_OFF = NORM_OFF + 2 * NKV * 4;
-  static constexpr int ROW_OFF = INV_OFF + M * 4;
+  static constexpr int MAX_OFF = NORM_OFF + 2 * NKV * 4;  // [2][2][M]: the halves' row maxima, later sums
+  static constexpr int ROW_OFF = MAX_OFF + 4 * M * 4;
   static constexpr int BYTES = ROW_OFF + M * static_cast<int>(sizeof(RowInfo));
   // At least half the SM's shared memory: one CTA, and its 512 TMEM columns, per SM.
   static constexpr int SMEM = (BYTES + 1024 > 120 * 1024 ? BYTES + 1024 : 120 * 1024);
-  static constexpr int THREADS = 512;
-  static constexpr int WIDEN = 256;                 // threads of the widening role
+  static constexpr int SOFT = 256, WIDEN = 256;     // threads of the softmax and widening roles
+  static constexpr int THREADS = SOFT + WIDEN + 128;  // the MMA warp, in a warpgroup of its own
+  // Registers per thread of the roles: 5 warpgroups are launched with 96 each.
+  static constexpr int REG_SOFT = 136, REG_WIDEN = 88, REG_MMA = 32;
+  static_assert(2 * REG_SOFT + 2 * REG_WIDEN + REG_MMA <= 5 * 96, "the roles share the launch's registers");
   // Output staging of the epilogue: RP rows at a time, padded by 16 bytes.
   static constexpr int STRIDE = D + 4;
   static constexpr int RP = 64 * STRIDE * 4 <= LUT_OFF ? 64 : 32;
@@ -74,8 +77,25 @@ struct CTiles {
 
 }  // namespace
 
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// umma_f16 on the low words of two 128-byte-swizzle descriptors (their high
+// words are the same constant: row-group stride, version, layout).
+__device__ __forceinline__ uint32_t umma_lo(uint32_t smem_addr) { return ((smem_addr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ void umma_f16_lo(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                            bool accumulate) {
+  constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(kHi));
+}
+
 template <int D, int B, int ROT>
-__global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a) {
+__global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a) {
   using C = CTiles<D, B, ROT>;
   constexpr int M = C::M, NKV = C::NKV, CW = C::CW, NCH = C::NCH, NS = C::NS, NSLOT = C::NSLOT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -91,7 +111,7 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
   uint8_t* const ring = smem + C::RING_OFF;
   uint32_t* const sLut = reinterpret_cast<uint32_t*>(smem + C::LUT_OFF);
   float* const sNorm = reinterpret_cast<float*>(smem + C::NORM_OFF);
-  float* const sInv = reinterpret_cast<float*>(smem + C::INV_OFF);
+  float* const sMax = reinterpret_cast<float*>(smem + C::MAX_OFF);
   RowInfo* const sRow = reinterpret_cast<RowInfo*>(smem + C::ROW_OFF);
 
   const int G = a.n_q_heads / a.n_kv_heads;
@@ -112,9 +132,9 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&b_sfull[s], 1);
-      mbar_init(&b_sfree[s], 4);
+      mbar_init(&b_sfree[s], C::SOFT / 32);
     }
-    mbar_init(&b_pfull, 4);
+    mbar_init(&b_pfull, C::SOFT / 32);
     mbar_init(&b_pvdone, 1);
     mbar_init(&b_tail, 1);
     s_abort = 0;
@@ -136,9 +156,9 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
   scored_lengths(a, b, tid == 0, seqlen, n);
   const int base = seqlen - n;
   const bool tree = a.tree != nullptr;
-  if (tid >= 448) scored_depths(a, b, n, tid - 448, s_depth);
-  RowInfo row{0, 0, 0, 0.0f, 0ull};
+  if (tid >= 128 && tid < 192) scored_depths(a, b, n, tid - 128, s_depth);
   if (tid < M) {
+    RowInfo row{0, 0, 0, 0.0f, 0ull};
     if (tid < rows) row = scored_row(a, b, kvh, q0 * G + tid, seqlen, n);
     sRow[tid] = row;
     const bool some = row.lo < row.hi;
@@ -194,204 +214,28 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
     }
   };
 
-  float m_used = -INFINITY, l_sum = 0.0f;
-  float otail[C::OR > 0 ? C::OR : 1];
-  const uint32_t row_tmem = tmem + ((uint32_t)(warp & 3) * 32u << 16);
-
-  if (warp < 4) {
-    // ------------------------------------------------------------- softmax --
-#pragma unroll
-    for (int i = 0; i < (C::OR > 0 ? C::OR : 1); ++i) otail[i] = 0.0f;
-    auto load_norm = [&](int step) {  // threads 0..63
-      const int64_t pos = (int64_t)(s0 + step) * NKV + tid;
-      return (!ROT && tid < NKV && step < n_steps && pos < seqlen)
-                 ? __half2float(*reinterpret_cast<const __half*>(stream + pos / kTile * C::REC + v_norm_offset(D, B) +
-                                                                 2 * (pos % kTile)))
-                 : 0.0f;
-    };
-    auto add_tail = [&](int step) {  // the last output dims of a step's P' C
-      if constexpr (C::OR > 0) {
-        wait(&b_tail, step);
-        tc_fence_after();
-#pragma unroll
-        for (int h = 0; h < C::OR; h += 32) {
-          uint32_t tv[32];
-          tmem_ld32(row_tmem + h, tv);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) otail[h + i] += __uint_as_float(tv[i]);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b_sfree[0]);
-      }
-    };
-    float nrm = load_norm(0);
-    for (int i = 0; i < n_steps; ++i) {
-      const int buf = i % NS;
-      if constexpr (!ROT) {
-        if (tid < NKV) sNorm[(i & 1) * NKV + tid] = nrm;
-        named_bar(1, 128);
-        nrm = load_norm(i + 1);
-      }
-      if (i > 0) add_tail(i - 1);
-      wait(&b_sfull[buf], i / NS);
-      tc_fence_after();
-      // Logits of 32 columns at a time. At D = 512 the registers hold the tail
-      // dims, so the logits go back to S's columns until their exponentials.
-      constexpr bool KEEP = C::OR == 0;
-      float x[KEEP ? 2 : 1][32];
-      const int pos0 = (s0 + i) * NKV;
-      uint64_t see = row.hi > 0 ? ~0ull : 0ull;
-      if (pos0 < flo || pos0 + NKV > fhi) see = scored_step_bits(row, tree, base, pos0);
-      const bool masked = __any_sync(0xffffffffu, see != ~0ull);
-      float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float (&v)[32] = x[KEEP ? h : 0];
-        uint32_t sv[32];
-        tmem_ld32(row_tmem + 64 * buf + 32 * h, sv);
-        tmem_ld_wait();
-        if (KEEP && h == 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&b_sfree[buf]);
-        }
-        if (a.cap_log2 == 0.0f) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(sv[j]) * a.mul;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = a.cap_log2 * tanh_f32(__uint_as_float(sv[j]) * a.mul);
-        }
-        if (a.slopes) {
-          const int p0 = pos0 + 32 * h;
-          if (tree && p0 + 32 > base) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              v[j] = fmaf(-row.slope, static_cast<float>(abs(row.at - scored_key_at(s_depth, tree, base, p0 + j))), v[j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = fmaf(-row.slope, static_cast<float>(abs(row.at - p0 - j)), v[j]);
-          }
-        }
-        if (masked) {
-          const uint32_t bits = static_cast<uint32_t>(see >> (32 * h));
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = (bits >> j & 1u) ? v[j] : -INFINITY;
-        }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], v[j]);
-        if constexpr (!KEEP) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) sv[j] = __float_as_uint(v[j]);
-          tmem_st32(row_tmem + 64 * buf + 32 * h, sv);
-        }
-      }
-      if constexpr (!KEEP) tmem_st_wait();
-      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      // P' and (for a rescale) O are free once the step before has been multiplied.
-      if (i > 0) wait(&b_pvdone, i - 1);
-      tc_fence_after();
-      const bool need = mx > m_used + 2.0f;  // also when m_used is -inf and a key is seen
-      if (__any_sync(0xffffffffu, need)) {
-        const float f = need ? ((m_used == -INFINITY) ? 0.0f : fast_exp2(m_used - mx)) : 1.0f;
-        if (i > 0) {
-#pragma unroll 1
-          for (int c0 = C::OCOL; c0 < C::OCOL + C::OT; c0 += 32) {
-            uint32_t ov[32];
-            tmem_ld32(row_tmem + c0, ov);
-            tmem_ld_wait();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
-            tmem_st32(row_tmem + c0, ov);
-          }
-          tmem_st_wait();
-        }
-#pragma unroll
-        for (int k = 0; k < C::OR; ++k) otail[k] *= f;
-        l_sum *= f;
-        if (need) m_used = mx;
-      }
-      const float mref = (m_used == -INFINITY) ? 0.0f : m_used;  // nothing seen yet: every x is -inf
-      float ps[2] = {0.0f, 0.0f};
-      const float4* n4 = reinterpret_cast<const float4*>(sNorm + (i & 1) * NKV);
-#pragma unroll
-      for (int c = 0; c < NKV / 8; ++c) {
-        float (&v)[32] = x[KEEP ? c / 4 : 0];
-        if constexpr (!KEEP) {
-          if (c % 4 == 0) {
-            uint32_t sv[32];
-            tmem_ld32(row_tmem + 64 * buf + 8 * c, sv);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(sv[j]);
-          }
-        }
-        float y[8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int j = 8 * (c % 4) + 4 * h;
-          const float p0 = fast_exp2(v[j] - mref), p1 = fast_exp2(v[j + 1] - mref);
-          const float p2 = fast_exp2(v[j + 2] - mref), p3 = fast_exp2(v[j + 3] - mref);
-          ps[h] += (p0 + p1) + (p2 + p3);
-          if constexpr (ROT) {
-            y[4 * h] = p0, y[4 * h + 1] = p1, y[4 * h + 2] = p2, y[4 * h + 3] = p3;
-          } else {  // the norm of a key that the row does not see may hold any bytes
-            const float4 nn = n4[2 * c + h];
-            y[4 * h] = p0 > 0.0f ? p0 * nn.x : 0.0f;
-            y[4 * h + 1] = p1 > 0.0f ? p1 * nn.y : 0.0f;
-            y[4 * h + 2] = p2 > 0.0f ? p2 * nn.z : 0.0f;
-            y[4 * h + 3] = p3 > 0.0f ? p3 * nn.w : 0.0f;
-          }
-        }
-        uint32_t hi[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) hi[k] = pack_half2(y[2 * k], y[2 * k + 1]);
-        *reinterpret_cast<uint4*>(sP + sw128_offset(tid, 8 * c, M)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if constexpr (C::PSPLIT) {
-          uint32_t lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __half2 hh = *reinterpret_cast<const __half2*>(&hi[k]);
-            lo[k] = pack_half2(y[2 * k] - __low2float(hh), y[2 * k + 1] - __high2float(hh));
-          }
-          *reinterpret_cast<uint4*>(sP + C::P_BYTES + sw128_offset(tid, 8 * c, M)) =
-              make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
-      l_sum += ps[0] + ps[1];
-      fence_proxy_async();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b_pfull);
-    }
-    if (n_steps > 0) {
-      add_tail(n_steps - 1);
-      wait(&b_pvdone, n_steps - 1);
-      tc_fence_after();
-    }
-    sInv[tid] = l_sum > 0.0f ? 1.0f / l_sum : 0.0f;
-  } else if (warp < 12) {
+  if (tid >= C::SOFT && tid < C::SOFT + C::WIDEN) {
     // ------------------------------------------------------------ widening --
-    const int wt = tid - 128;  // 0 .. 255
-    int q = 0;                 // slots filled
-    auto slot_wait = [&](int k) {
-      if (k >= NSLOT) wait(&b_free[k % NSLOT], k / NSLOT - 1);
-    };
-    auto slot_done = [&](int k) {
+    regs_dec<C::REG_WIDEN>();
+    const int wt = tid - C::SOFT;  // 0 .. 255
+    int slot = 0;                  // the next slot to fill, and the parity of its last release
+    uint32_t turn = 1;             // (a slot's first use waits for the phase before its first: it passes at once)
+    auto slot_done = [&]() {
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&b_full[k % NSLOT]);
+      if (lane == 0) mbar_arrive(&b_full[slot]);
+      if (++slot == NSLOT) slot = 0, turn ^= 1u;
     };
     // K chunk c of a step: 4 records x CW / 32 blocks x 32 lanes of 16 bytes,
     // each 8 dims of tokens kpp and kpp + 8 of a record.
     constexpr int PIECES = 4 * (CW / 32) * 32, KR = PIECES / C::WIDEN;
     static_assert(KR >= 1 && PIECES % C::WIDEN == 0, "K pieces per thread");
     const int kq = lane >> 3, kpp = lane & 7;
-    uint4 kw[KR];
-    uint32_t ks[KR];  // the two tokens' scales
-    auto fetch_k = [&](int step, int c) {
+    // Codes are fetched two chunks ahead (one, of a whole step, where a step has one chunk).
+    constexpr int AHEAD = NCH > 1 ? 2 : 1;
+    uint4 kw_[AHEAD][KR];
+    uint32_t ks_[AHEAD][KR];  // the two tokens' scales
+    auto fetch_k = [&](int step, int c, uint4 (&kw)[KR], uint32_t (&ks)[KR]) {
       if (step >= n_steps) return;
 #pragma unroll
       for (int r = 0; r < KR; ++r) {
@@ -409,17 +253,17 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
         }
       }
     };
-    auto widen_k = [&](int step, int c) {
+    auto widen_k = [&](int step, int c, uint4 (&kw)[KR], uint32_t (&ks)[KR]) {
       uint4 w4[KR];
       uint32_t sc[KR];
 #pragma unroll
       for (int r = 0; r < KR; ++r) w4[r] = kw[r], sc[r] = ks[r];
-      if (c + 1 < NCH) fetch_k(step, c + 1);
-      else fetch_k(step + 1, 0);
-      slot_wait(q);
-      slot_wait(q + 1);
-      uint8_t* const s_hi = ring + (q % NSLOT) * C::SLOT;
-      uint8_t* const s_lo = ring + ((q + 1) % NSLOT) * C::SLOT;
+      if (c + AHEAD < NCH) fetch_k(step, c + AHEAD, kw, ks);
+      else fetch_k(step + 1, c + AHEAD - NCH, kw, ks);
+      // hi is handed over before lo is stored.
+      uint4 lo4[KR][2];
+      wait(&b_free[slot], turn);
+      uint8_t* dst = ring + slot * C::SLOT;
 #pragma unroll
       for (int r = 0; r < KR; ++r) {
         const int u = r * 8 + (wt >> 5);
@@ -427,8 +271,7 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
         const uint32_t w[4] = {w4[r].x, w4[r].y, w4[r].z, w4[r].w};
 #pragma unroll
         for (int hs = 0; hs < 2; ++hs) {
-          const uint32_t d1 = hs ? sc[r] >> 16 : sc[r] & 0xffffu;
-          const uint32_t dd = d1 | d1 << 16;
+          const uint32_t dd = __byte_perm(sc[r], 0u, hs ? 0x3232 : 0x1010);
           const __half2 d2 = *reinterpret_cast<const __half2*>(&dd);
           uint32_t qh[4], hi[4], lo[4];
           i8x4_to_half2x2(w[2 * hs], qh[0], qh[1]);
@@ -441,14 +284,22 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
             hi[e] = *reinterpret_cast<const uint32_t*>(&h);
             lo[e] = *reinterpret_cast<const uint32_t*>(&l);
           }
-          const uint32_t off = sw128_offset(row0 + 8 * hs, k0, NKV);
-          *reinterpret_cast<uint4*>(s_hi + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(s_lo + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *reinterpret_cast<uint4*>(dst + sw128_offset(row0 + 8 * hs, k0, NKV)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          lo4[r][hs] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
-      slot_done(q);
-      slot_done(q + 1);
-      q += 2;
+      slot_done();
+      wait(&b_free[slot], turn);
+      dst = ring + slot * C::SLOT;
+#pragma unroll
+      for (int r = 0; r < KR; ++r) {
+        const int u = r * 8 + (wt >> 5);
+        const int row0 = u / (CW / 32) * kTile + kpp, k0 = (u % (CW / 32)) * 32 + 8 * kq;
+#pragma unroll
+        for (int hs = 0; hs < 2; ++hs)
+          *reinterpret_cast<uint4*>(dst + sw128_offset(row0 + 8 * hs, k0, NKV)) = lo4[r][hs];
+      }
+      slot_done();
     };
     // V chunk c of a step: units of (lane stream, 8 dims), 16 fields of 2B
     // bits in B words of the stream. Unit v = 16 (...) + 4 record + (stream % 4).
@@ -459,9 +310,9 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
     const bool v_on = wt < UNITS;
     const int v_rec = (wt >> 2) & 3, v_t = wt & 3, v_part = wt >> 4;  // 8-dim part of the chunk
     constexpr int GR = v_granule(D, B);
-    uint32_t vw[B], vn[2] = {0u, 0u};
+    uint32_t vw_[AHEAD][B], vn_[AHEAD][2];
     auto v_chunk = [&](int k) { return C::OR > 0 ? (k + NCH - 1) % NCH : k; };  // D = 512: the tail's chunk first
-    auto fetch_v = [&](int step, int k) {
+    auto fetch_v = [&](int step, int k, uint32_t (&vw)[B], uint32_t (&vn)[2]) {
       if (step >= n_steps || !v_on) return;
       const int part = v_chunk(k) * (CW / 8) + v_part;  // dims 8 part .. 8 part + 7
       const int L = 4 * (part / SUB) + v_t, w0 = (part % SUB) * B;
@@ -479,12 +330,12 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
         vn[1] = rec < n_rec ? *reinterpret_cast<const uint32_t*>(nb + 16) : 0u;
       }
     };
-    auto widen_v = [&](int step, int k) {
-      uint32_t w[B], nn[2] = {vn[0], vn[1]};
+    auto widen_v = [&](int step, int k, uint32_t (&vw)[B], uint32_t (&vn)[2]) {
+      uint32_t w[B], nn[2] = {ROT ? vn[0] : 0u, ROT ? vn[1] : 0u};
 #pragma unroll
       for (int e = 0; e < B; ++e) w[e] = vw[e];
-      if (k + 1 < NCH) fetch_v(step, k + 1);
-      else fetch_v(step + 1, 0);
+      if (k + AHEAD < NCH) fetch_v(step, k + AHEAD, vw, vn);
+      else fetch_v(step + 1, k + AHEAD - NCH, vw, vn);
       if constexpr (ROT) {
         const int pos0 = (s0 + step) * NKV;
         if (pos0 < flo || pos0 + NKV > fhi) {  // norms of positions that no row sees may hold any bytes
@@ -500,8 +351,8 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
           nn[1] &= (mb & 1u ? 0xffffu : 0u) | (mb & 2u ? 0xffff0000u : 0u);
         }
       }
-      slot_wait(q);
-      uint8_t* const dst = ring + (q % NSLOT) * C::SLOT;
+      wait(&b_free[slot], turn);
+      uint8_t* const dst = ring + slot * C::SLOT;
       if (v_on) {
         const uint32_t lut = smem_u32(sLut) + (uint32_t)(lane << 2);
         const int tok = v_rec * kTile + 2 * v_t;
@@ -533,84 +384,306 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
           *reinterpret_cast<uint32_t*>(dst + sw128_offset(dim, tok + (flip ? 0 : 8), CW)) = flip ? lo : hi;
         }
       }
-      slot_done(q);
-      ++q;
+      slot_done();
     };
-    fetch_k(0, 0);
-    fetch_v(0, 0);
+#pragma unroll
+    for (int c = 0; c < AHEAD; ++c) {
+      fetch_k(0, c, kw_[c], ks_[c]);
+      fetch_v(0, c, vw_[c], vn_[c]);
+    }
     auto all_k = [&](int step) {
-      for (int c = 0; c < NCH; ++c) widen_k(step, c);
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) widen_k(step, c, kw_[c % AHEAD], ks_[c % AHEAD]);
     };
     if (NS == 2 && n_steps > 0) all_k(0);
     for (int i = 0; i < n_steps; ++i) {
       if constexpr (NS == 1) all_k(i);
       else if (i + 1 < n_steps) all_k(i + 1);
-      for (int k = 0; k < NCH; ++k) widen_v(i, k);
+#pragma unroll
+      for (int k = 0; k < NCH; ++k) widen_v(i, k, vw_[k % AHEAD], vn_[k % AHEAD]);
     }
-  } else {
-    if (warp == 12 && lane == 0) {
-      // --------------------------------------------------------------- MMA --
-      const uint32_t q_base = smem_u32(sQ), p_base = smem_u32(sP), r_base = smem_u32(ring);
-      int q = 0;
-      auto s_step = [&](int i) {
-        const int buf = i % NS;
-        if (i >= NS) wait(&b_sfree[buf], i / NS - 1);
-        for (int c = 0; c < 2 * NCH; ++c) {  // chunk c / 2, hi then lo
-          wait(&b_full[q % NSLOT], q / NSLOT);
-          tc_fence_after();
-          const uint32_t slot = r_base + (q % NSLOT) * C::SLOT;
+    return;
+  }
+
+  if (tid >= C::SOFT + C::WIDEN) {
+    // ----------------------------------------------------------------- MMA --
+    regs_dec<C::REG_MMA>();
+    if (warp > (C::SOFT + C::WIDEN) / 32) return;
+    // The whole warp walks the schedule and one lane issues, so that the
+    // operand descriptors stay in uniform registers: their low words advance
+    // by constants from the operands' bases.
+    const uint32_t q_lo = umma_lo(smem_u32(sQ)), p_lo = umma_lo(smem_u32(sP)), r_lo = umma_lo(smem_u32(ring));
+    constexpr uint32_t kS = umma_idesc_f16_f32(M, NKV);
+    const bool lead = lane == 0;
+    int slot = 0;
+    uint32_t turn = 0;
+    auto slot_next = [&]() {
+      if (lead) umma_commit(&b_free[slot]);
+      if (++slot == NSLOT) slot = 0, turn ^= 1u;
+    };
+    auto s_step = [&](int i) {
+      const int buf = i % NS;
+      if (i >= NS) wait(&b_sfree[buf], i / NS - 1);
 #pragma unroll
-          for (int ks = 0; ks < CW / 16; ++ks) {
-            const int kd = (c >> 1) * (CW / 16) + ks;
-            umma_f16(tmem + 64 * buf, umma_desc_sw128(q_base + (kd >> 2) * (M * 128) + (kd & 3) * 32),
-                     umma_desc_sw128(slot + (ks >> 2) * (NKV * 128) + (ks & 3) * 32), umma_idesc_f16_f32(M, NKV),
-                     c > 0 || ks > 0);
+      for (int c = 0; c < NCH; ++c) {
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {  // hi, lo
+          wait(&b_full[slot], turn);
+          tc_fence_after();
+          const uint32_t s_lo = r_lo + slot * (C::SLOT >> 4);
+          if (lead) {
+#pragma unroll
+            for (int ks = 0; ks < CW / 16; ++ks) {
+              const int kd = c * (CW / 16) + ks;
+              umma_f16_lo(tmem + 64 * buf, q_lo + (((kd >> 2) * (M * 128) + (kd & 3) * 32) >> 4),
+                          s_lo + (((ks >> 2) * (NKV * 128) + (ks & 3) * 32) >> 4), kS, c > 0 || part > 0 || ks > 0);
+            }
           }
-          umma_commit(&b_free[q % NSLOT]);
-          ++q;
+          slot_next();
         }
-        umma_commit(&b_sfull[buf]);
-      };
-      // O columns [col, col + N) += P' C over the step's 64 tokens, C rows from `dims`.
-      auto pv = [&](uint32_t col, uint32_t dims, uint32_t idesc, bool keep) {
+      }
+      if (lead) umma_commit(&b_sfull[buf]);
+    };
+    // O columns [col, col + N) += P' C over the step's 64 tokens, C rows from descriptor `dims`.
+    auto pv = [&](uint32_t col, uint32_t dims, uint32_t idesc, bool keep) {
 #pragma unroll
-        for (int ks = 0; ks < NKV / 16; ++ks) {
-          const uint64_t bd = umma_desc_sw128(dims + ks * 32);
-          umma_f16(tmem + col, umma_desc_sw128(p_base + ks * 32), bd, idesc, keep || ks > 0);
-          if constexpr (C::PSPLIT) umma_f16(tmem + col, umma_desc_sw128(p_base + C::P_BYTES + ks * 32), bd, idesc, true);
-        }
-      };
-      auto pv_step = [&](int i) {
-        wait(&b_pfull, i);
+      for (int ks = 0; ks < NKV / 16; ++ks) {
+        umma_f16_lo(tmem + col, p_lo + 2 * ks, dims + 2 * ks, idesc, keep || ks > 0);
+        if constexpr (C::PSPLIT)
+          umma_f16_lo(tmem + col, p_lo + (C::P_BYTES >> 4) + 2 * ks, dims + 2 * ks, idesc, true);
+      }
+    };
+    auto pv_step = [&](int i) {
+      wait(&b_pfull, i);
+#pragma unroll
+      for (int k = 0; k < NCH; ++k) {
+        wait(&b_full[slot], turn);
         tc_fence_after();
-        for (int k = 0; k < NCH; ++k) {
-          wait(&b_full[q % NSLOT], q / NSLOT);
-          tc_fence_after();
-          const uint32_t slot = r_base + (q % NSLOT) * C::SLOT;
+        const uint32_t s_lo = r_lo + slot * (C::SLOT >> 4);
+        if (lead) {
           if constexpr (C::OR > 0) {
             if (k == 0) {  // the last chunk: its upper half to S's columns, its lower half to O
-              pv(0, slot + C::OR * 128, umma_idesc_f16_f32(M, C::OR), false);
+              pv(0, s_lo + (C::OR * 128 >> 4), umma_idesc_f16_f32(M, C::OR), false);
               umma_commit(&b_tail);
-              pv(C::OCOL + D - CW, slot, umma_idesc_f16_f32(M, CW - C::OR), i > 0);
+              pv(C::OCOL + D - CW, s_lo, umma_idesc_f16_f32(M, CW - C::OR), i > 0);
             } else {
-              pv(C::OCOL + (k - 1) * CW, slot, umma_idesc_f16_f32(M, CW), i > 0);
+              pv(C::OCOL + (k - 1) * CW, s_lo, umma_idesc_f16_f32(M, CW), i > 0);
             }
           } else {
-            pv(C::OCOL + k * CW, slot, umma_idesc_f16_f32(M, CW), i > 0);
+            pv(C::OCOL + k * CW, s_lo, umma_idesc_f16_f32(M, CW), i > 0);
           }
-          umma_commit(&b_free[q % NSLOT]);
-          ++q;
         }
-        umma_commit(&b_pvdone);
-      };
-      if (NS == 2 && n_steps > 0) s_step(0);
-      for (int i = 0; i < n_steps; ++i) {
-        if constexpr (NS == 1) s_step(i);
-        else if (i + 1 < n_steps) s_step(i + 1);
-        pv_step(i);
+        slot_next();
       }
+      if (lead) umma_commit(&b_pvdone);
+    };
+    if (NS == 2 && n_steps > 0) s_step(0);
+    for (int i = 0; i < n_steps; ++i) {
+      if constexpr (NS == 1) s_step(i);
+      else if (i + 1 < n_steps) s_step(i + 1);
+      pv_step(i);
     }
     __syncwarp();
+    return;
+  }
+
+  // --------------------------------------------------------------- softmax --
+  regs_inc<C::REG_SOFT>();
+  // Softmax state: row tid % 128, columns [32 half, 32 half + 32) of every step.
+  float m_used = -INFINITY, l_sum = 0.0f;
+  constexpr int ORH = C::OR / 2;  // tail dims per thread
+  float otail[C::OR > 0 ? ORH : 1];
+  const int half = warp >> 2, rowi = tid & (M - 1);
+  const uint32_t row_tmem = tmem + ((uint32_t)(warp & 3) * 32u << 16);
+
+  {
+    const RowInfo row = sRow[rowi];
+#pragma unroll
+    for (int i = 0; i < (C::OR > 0 ? ORH : 1); ++i) otail[i] = 0.0f;
+    auto load_norm = [&](int step) {  // threads 0..63
+      const int64_t pos = (int64_t)(s0 + step) * NKV + tid;
+      return (!ROT && tid < NKV && step < n_steps && pos < seqlen)
+                 ? __half2float(*reinterpret_cast<const __half*>(stream + pos / kTile * C::REC + v_norm_offset(D, B) +
+                                                                 2 * (pos % kTile)))
+                 : 0.0f;
+    };
+    auto add_tail = [&](int step) {  // the last output dims of a step's P' C
+      if constexpr (C::OR > 0) {
+        wait(&b_tail, step);
+        tc_fence_after();
+        uint32_t tv[32];
+        tmem_ld32(row_tmem + ORH * half, tv);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_sfree[0]);
+#pragma unroll
+        for (int i = 0; i < ORH; ++i) otail[i] += __uint_as_float(tv[i]);
+      }
+    };
+    constexpr int kFormPlain = 0, kFormCap = 1, kFormAny = 2;
+    const int form = a.slopes || a.cap_log2 > kShortCap || (a.cap_log2 == 0.0f && a.mul <= 0.0f) ? kFormAny
+                     : a.cap_log2 > 0.0f                                                         ? kFormCap
+                                                                                                 : kFormPlain;
+    const float zA = form == kFormAny ? 1.0f : form == kFormCap ? -2.0f * a.cap_log2 : a.mul;
+    const float zC = form == kFormCap ? a.cap_log2 : 0.0f;
+    float nrm = load_norm(0);
+    for (int i = 0; i < n_steps; ++i) {
+      const int buf = i % NS;
+      if constexpr (!ROT) {
+        if (tid < NKV) sNorm[(i & 1) * NKV + tid] = nrm;
+        nrm = load_norm(i + 1);
+      }
+      if (i > 0) add_tail(i - 1);
+      wait(&b_sfull[buf], i / NS);
+      tc_fence_after();
+      uint32_t sv[32];
+      tmem_ld32(row_tmem + 64 * buf + 32 * half, sv);
+      tmem_ld_wait();
+      if constexpr (C::OR == 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_sfree[buf]);
+      }
+      // z of each key, with the logit = A z + C: S itself, the 1 / (1 + e^2x) of
+      // a short cap, or (distance bias, long cap, negative scale) the logit.
+      float z[32], mx;
+      const int p0 = (s0 + i) * NKV + 32 * half;
+      const int step0 = (s0 + i) * NKV;
+      uint32_t see = row.hi > 0 ? ~0u : 0u;
+      if (step0 < flo || step0 + NKV > fhi) see = static_cast<uint32_t>(scored_step_bits(row, tree, base, p0));
+      const bool masked = __any_sync(0xffffffffu, see != ~0u);
+      if (form == kFormCap) {
+        const uint64_t k2 = f32x2(a.mul * 2.8853900817779268f, a.mul * 2.8853900817779268f), one = f32x2(1.0f, 1.0f);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          const float2 y = f32x2_get(mul_f32x2(f32x2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), k2));
+          const float2 d = f32x2_get(add_f32x2(f32x2(fast_exp2(y.x), fast_exp2(y.y)), one));
+          z[j] = fast_rcp(d.x);
+          z[j + 1] = fast_rcp(d.y);
+        }
+      } else if (form == kFormPlain) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(sv[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z[j] = scored_logit(__uint_as_float(sv[j]), a.mul, a.cap_log2);
+        if (tree && p0 + 32 > base) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            z[j] = fmaf(-row.slope, static_cast<float>(abs(row.at - scored_key_at(s_depth, tree, base, p0 + j))), z[j]);
+        } else {
+          const float d0 = static_cast<float>(row.at - p0);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) z[j] = fmaf(-row.slope, fabsf(d0 - static_cast<float>(j)), z[j]);
+        }
+      }
+      if (masked) {
+        const float never = form == kFormCap ? INFINITY : -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z[j] = (see >> j & 1u) ? z[j] : never;
+      }
+      if (form == kFormCap) {
+        float t0 = z[0], t1 = z[1];
+#pragma unroll
+        for (int j = 2; j < 32; j += 4) {
+          t0 = min3(t0, z[j], z[j + 1]);
+          if (j + 2 < 32) t1 = min3(t1, z[j + 2], z[j + 3]);
+        }
+        mx = fmaf(zA, fminf(t0, t1), zC);
+      } else {
+        float t0 = z[0], t1 = z[1];
+#pragma unroll
+        for (int j = 2; j < 32; j += 4) {
+          t0 = max3(t0, z[j], z[j + 1]);
+          if (j + 2 < 32) t1 = max3(t1, z[j + 2], z[j + 3]);
+        }
+        mx = zA * fmaxf(t0, t1);
+      }
+      float* const ex = sMax + (i & 1) * 2 * M + rowi;
+      ex[half * M] = mx;
+      named_bar(1, C::SOFT);
+      mx = fmaxf(mx, ex[(1 - half) * M]);
+      // P' and (for a rescale) O are free once the step before has been multiplied.
+      if (i > 0) wait(&b_pvdone, i - 1);
+      tc_fence_after();
+      const bool need = mx > m_used + 2.0f;  // also when m_used is -inf and a key is seen
+      if (__any_sync(0xffffffffu, need)) {
+        const float f = need ? ((m_used == -INFINITY) ? 0.0f : fast_exp2(m_used - mx)) : 1.0f;
+        if (i > 0) {
+#pragma unroll 1
+          for (int c0 = C::OCOL + half * (C::OT / 2); c0 < C::OCOL + (half + 1) * (C::OT / 2); c0 += 32) {
+            uint32_t ov[32];
+            tmem_ld32(row_tmem + c0, ov);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * f);
+            tmem_st32(row_tmem + c0, ov);
+          }
+          tmem_st_wait();
+        }
+#pragma unroll
+        for (int k = 0; k < ORH; ++k) otail[k] *= f;
+        l_sum *= f;
+        if (need) m_used = mx;
+      }
+      const float mref = (m_used == -INFINITY) ? 0.0f : m_used;  // nothing seen yet: every x is -inf
+      uint64_t ps = f32x2(0.0f, 0.0f);
+      const uint64_t zA2 = f32x2(zA, zA), zC2 = f32x2(zC - mref, zC - mref);
+      const float4* n4 = reinterpret_cast<const float4*>(sNorm + (i & 1) * NKV + 32 * half);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int j = 8 * c + 4 * h;
+          const float2 xa = f32x2_get(fma_f32x2(zA2, f32x2(z[j], z[j + 1]), zC2));
+          const float2 xb = f32x2_get(fma_f32x2(zA2, f32x2(z[j + 2], z[j + 3]), zC2));
+          uint64_t ya = f32x2(fast_exp2(xa.x), fast_exp2(xa.y)), yb = f32x2(fast_exp2(xb.x), fast_exp2(xb.y));
+          ps = add_f32x2(ps, add_f32x2(ya, yb));
+          if constexpr (!ROT) {
+            float4 nn = n4[2 * c + h];
+            if (masked) {  // the norm of a key that the row does not see may hold any bytes
+              nn.x = (see >> j & 1u) ? nn.x : 0.0f;
+              nn.y = (see >> (j + 1) & 1u) ? nn.y : 0.0f;
+              nn.z = (see >> (j + 2) & 1u) ? nn.z : 0.0f;
+              nn.w = (see >> (j + 3) & 1u) ? nn.w : 0.0f;
+            }
+            ya = mul_f32x2(ya, f32x2(nn.x, nn.y));
+            yb = mul_f32x2(yb, f32x2(nn.z, nn.w));
+          }
+          const float2 fa = f32x2_get(ya), fb = f32x2_get(yb);
+          hi[2 * h] = pack_half2(fa.x, fa.y);
+          hi[2 * h + 1] = pack_half2(fb.x, fb.y);
+          if constexpr (C::PSPLIT) {
+            const float2 ha = __half22float2(*reinterpret_cast<const __half2*>(&hi[2 * h]));
+            const float2 hb = __half22float2(*reinterpret_cast<const __half2*>(&hi[2 * h + 1]));
+            lo[2 * h] = pack_half2(fa.x - ha.x, fa.y - ha.y);
+            lo[2 * h + 1] = pack_half2(fb.x - hb.x, fb.y - hb.y);
+          }
+        }
+        const uint32_t off = sw128_offset(rowi, 32 * half + 8 * c, M);
+        *reinterpret_cast<uint4*>(sP + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if constexpr (C::PSPLIT)
+          *reinterpret_cast<uint4*>(sP + C::P_BYTES + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      const float2 p2 = f32x2_get(ps);
+      l_sum += p2.x + p2.y;
+      fence_proxy_async();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b_pfull);
+    }
+    if (n_steps > 0) {
+      add_tail(n_steps - 1);
+      wait(&b_pvdone, n_steps - 1);
+      tc_fence_after();
+    }
+    // The row's sum: both halves'.
+    float* const ex = sMax + (n_steps & 1) * 2 * M + rowi;
+    ex[half * M] = l_sum;
+    named_bar(1, C::SOFT);
+    l_sum += ex[(1 - half) * M];
   }
 
   // ---------------------------------------------------------------- epilogue --
@@ -620,20 +693,20 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
   const bool direct = a.n_split == 1;
   float* const slot = a.part + (int64_t)blockIdx.x * (M * (D + 1));
   float* const stage = reinterpret_cast<float*>(smem);
-  if (warp < 4 && tid < rows) {
+  const float inv = l_sum > 0.0f ? 1.0f / l_sum : 0.0f;
+  if (tid < rows) {
     const float lse = l_sum > 0.0f ? (m_used + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
     if (direct) a.lse[((int64_t)b * a.n_q + q0 + tid / G) * a.n_q_heads + kvh * G + tid % G] = lse;
     else slot[(int64_t)M * D + tid] = lse;
   }
   tc_fence_before();
-  __syncthreads();
+  named_bar(1, C::SOFT);
   tc_fence_after();
   for (int r0 = 0; r0 < rows; r0 += C::RP) {
-    if (warp < 4 && warp * 32 >= r0 && warp * 32 < r0 + C::RP) {
-      const float inv = sInv[tid];
-      float* const dst = stage + (tid - r0) * C::STRIDE;
+    if ((warp & 3) * 32 >= r0 && (warp & 3) * 32 < r0 + C::RP) {
+      float* const dst = stage + (rowi - r0) * C::STRIDE;
 #pragma unroll 1
-      for (int c = 0; c < C::OT; c += 32) {
+      for (int c = half * (C::OT / 2); c < (half + 1) * (C::OT / 2); c += 32) {
         uint32_t ov[32];
         if (n_steps > 0) {
           tmem_ld32(row_tmem + C::OCOL + c, ov);
@@ -648,14 +721,14 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
       }
       if constexpr (C::OR > 0) {
 #pragma unroll
-        for (int k = 0; k < C::OR; k += 4)
-          *reinterpret_cast<float4*>(dst + C::OT + k) =
+        for (int k = 0; k < ORH; k += 4)
+          *reinterpret_cast<float4*>(dst + C::OT + ORH * half + k) =
               inv > 0.0f ? make_float4(otail[k] * inv, otail[k + 1] * inv, otail[k + 2] * inv, otail[k + 3] * inv)
                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
     }
-    __syncthreads();
-    for (int r = r0 + warp; r < min(rows, r0 + C::RP); r += C::THREADS / 32) {
+    named_bar(1, C::SOFT);
+    for (int r = r0 + warp; r < min(rows, r0 + C::RP); r += C::SOFT / 32) {
       float2 v[D / 64];
 #pragma unroll
       for (int e = 0; e < D / 64; ++e)
@@ -669,7 +742,7 @@ __global__ void __launch_bounds__(512, 1) attn_scored_tiles_kernel(ScoredArgs a)
         derotate_store_row<D>(v, lane, nullptr, slot + (int64_t)r * D);
       }
     }
-    __syncthreads();
+    named_bar(1, C::SOFT);
   }
   if (warp == 0) tmem_dealloc(tmem, 512);
 }

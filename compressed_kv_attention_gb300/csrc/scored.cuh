@@ -143,9 +143,20 @@ __device__ __forceinline__ float tanh_f32(float x) {
   return ax < 0.25f ? small : big;
 }
 
+// 1 - 2 / (1 + e^(2x)) alone: exact to about 4e-7 absolute, not relative, which
+// is all a logit needs while the cap is small: at caps up to 100 (kShortCap, in
+// log2 units) the logit is within 6e-5, and the probabilities within the
+// rounding of their fp16 form.
+constexpr float kShortCap = 144.3f;
+__device__ __forceinline__ float tanh_short(float x) {
+  return fmaf(-2.0f, fast_rcp(1.0f + fast_exp2(x * 2.8853900817779268f)), 1.0f);
+}
+
 // The row's logit for one raw product S, before its mask.
 __device__ __forceinline__ float scored_logit(float s, float mul, float cap_log2) {
-  return cap_log2 == 0.0f ? s * mul : cap_log2 * tanh_f32(s * mul);
+  return cap_log2 == 0.0f        ? s * mul
+         : cap_log2 <= kShortCap ? cap_log2 * tanh_short(s * mul)
+                                 : cap_log2 * tanh_f32(s * mul);
 }
 
 // Position of a key for the distance bias: a drafted key counts by its depth.
