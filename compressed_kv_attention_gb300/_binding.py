@@ -130,8 +130,8 @@ def _ptr(t) -> int:
 
 def _stream(stream) -> int:
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the raw handle: torch.cuda.current_stream() builds a Stream object, 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return int(stream.cuda_stream)
 
 
@@ -390,35 +390,49 @@ def attn_prefill_shared(prefix: PackedCache, n_prefix: int, k_tail, v_tail, tail
                                           workspace.numel(), _stream(stream)))
 
 
-def _dtype_code(t, what: str) -> int:
-    import torch
-    codes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-    if t.dtype not in codes:
-        raise TypeError(f"{what} must be float32, float16 or bfloat16, got {t.dtype}")
-    return codes[t.dtype]
+_DTYPES = None  # torch dtype -> ckv_dtype
 
 
-def _expect(t, what: str, shape, *dtypes):
-    """Optional device tensors of the scored calls: exact shape, a listed type, contiguous."""
-    if t is None:
-        return
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous():
+def _dtypes():
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+    return _DTYPES
+
+
+def _expect(t, what: str, shape, dtypes, dev: int):
+    """A device tensor of the scored calls: on the cache's device, of a listed type, exact shape, contiguous."""
+    if t.dtype not in dtypes or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous tensor of shape {tuple(shape)} and type "
-                         f"{' or '.join(map(str, dtypes))}, got {tuple(t.shape)}, {t.dtype}")
+                         f"{' or '.join(map(str, dtypes))} on the cache's device, got {tuple(t.shape)}, {t.dtype}, "
+                         f"{t.device}")
 
 
-def _scored_tensors(cache, seq_len, q, out, lse, q_len, slopes):
+def _cache_device(cache) -> int:
+    """The cache's device, which has to be the current one (its stream takes the launch)."""
     import torch
-    B, n_q, n_q_heads, D = q.shape
-    if (B, D) != (cache.batch, cache.head_dim):
-        raise ValueError(f"q is for {B} sequences and head dim {D}, the cache for {cache.batch} and {cache.head_dim}")
-    _expect(q, "q", q.shape, torch.float16, torch.bfloat16)
-    _expect(out, "out", q.shape, torch.float32, torch.float16, torch.bfloat16)
-    _expect(lse, "lse", (B, n_q, n_q_heads), torch.float32)
-    _expect(seq_len, "seq_len", (B,), torch.int32)
-    _expect(q_len, "q_len", (B,), torch.int32)
-    _expect(slopes, "slopes", (n_q_heads,), torch.float32)
-    return B, n_q, n_q_heads
+    dev = cache.data.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the cache is on {cache.data.device}, not on the current CUDA device")
+    return dev
+
+
+def _scored_tensors(cache, seq_len, q, out, lse, workspace, q_len, slopes):
+    import torch
+    dev, shape, f32, i32 = _cache_device(cache), q.shape, (torch.float32,), (torch.int32,)
+    if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.head_dim:
+        raise ValueError(f"q must be [{cache.batch}, n_q, n_q_heads, {cache.head_dim}] for this cache, got {tuple(shape)}")
+    _expect(q, "q", shape, (torch.float16, torch.bfloat16), dev)
+    _expect(out, "out", shape, _dtypes(), dev)
+    _expect(lse, "lse", shape[:3], f32, dev)
+    _expect(seq_len, "seq_len", shape[:1], i32, dev)
+    _expect(workspace, "workspace", workspace.shape, (torch.uint8,), dev)
+    if q_len is not None:
+        _expect(q_len, "q_len", shape[:1], i32, dev)
+    if slopes is not None:
+        _expect(slopes, "slopes", shape[2:3], f32, dev)
+    return dev, shape
 
 
 def attn_scored_workspace(cache: PackedCache, max_seq_len: int, n_q: int, n_q_heads: int, n_split: int = 0) -> int:
@@ -433,13 +447,16 @@ def attn_scored(cache: PackedCache, seq_len, max_seq_len: int, q, scale: float, 
     [batch]) and a document mask (doc_start int32 [batch, n_q]). q: fp16 or bf16 [batch, n_q, n_q_heads, D];
     out: float32, fp16 or bf16 like q; lse float32 [batch, n_q, n_q_heads]."""
     import torch
-    B, n_q, n_q_heads = _scored_tensors(cache, seq_len, q, out, lse, q_len, slopes)
-    _expect(prefix_len, "prefix_len", (B,), torch.int32)
-    _expect(doc_start, "doc_start", (B, n_q), torch.int32)
+    dev, shape = _scored_tensors(cache, seq_len, q, out, lse, workspace, q_len, slopes)
+    if prefix_len is not None:
+        _expect(prefix_len, "prefix_len", shape[:1], (torch.int32,), dev)
+    if doc_start is not None:
+        _expect(doc_start, "doc_start", shape[:2], (torch.int32,), dev)
     score = CkvScoreStruct(softcap, window, _ptr(slopes), _ptr(prefix_len), _ptr(doc_start))
-    _check(load().ckv_attn_scored(cache.ref(), _ptr(seq_len), max_seq_len, _ptr(q), _dtype_code(q, "q"), n_q,
-                                  n_q_heads, _ptr(q_len), scale, ctypes.byref(score), n_split, _ptr(out),
-                                  _dtype_code(out, "out"), _ptr(lse), _ptr(workspace), workspace.numel(),
+    codes = _dtypes()
+    _check(load().ckv_attn_scored(cache.ref(), seq_len.data_ptr(), max_seq_len, q.data_ptr(), codes[q.dtype], shape[1],
+                                  shape[2], _ptr(q_len), scale, ctypes.byref(score), n_split, out.data_ptr(),
+                                  codes[out.dtype], lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
                                   _stream(stream)))
 
 
@@ -453,13 +470,14 @@ def attn_tree(cache: PackedCache, seq_len, max_seq_len: int, tree_mask, q, scale
     sees the committed cache and the nodes whose bits are set in tree_mask[b, t] (int64 or uint64 [batch, n_q],
     its ancestors and itself). Tensors as attn_scored."""
     import torch
-    B, n_q, n_q_heads = _scored_tensors(cache, seq_len, q, out, lse, q_len, slopes)
-    _expect(tree_mask, "tree_mask", (B, n_q), torch.int64, torch.uint64)
+    dev, shape = _scored_tensors(cache, seq_len, q, out, lse, workspace, q_len, slopes)
+    _expect(tree_mask, "tree_mask", shape[:2], (torch.int64, torch.uint64), dev)
     score = CkvScoreStruct(softcap, window, _ptr(slopes), None, None)
-    _check(load().ckv_attn_tree(cache.ref(), _ptr(seq_len), max_seq_len, _ptr(tree_mask), _ptr(q),
-                                _dtype_code(q, "q"), n_q, n_q_heads, _ptr(q_len), scale, ctypes.byref(score), n_split,
-                                _ptr(out), _dtype_code(out, "out"), _ptr(lse), _ptr(workspace), workspace.numel(),
-                                _stream(stream)))
+    codes = _dtypes()
+    _check(load().ckv_attn_tree(cache.ref(), seq_len.data_ptr(), max_seq_len, tree_mask.data_ptr(), q.data_ptr(),
+                                codes[q.dtype], shape[1], shape[2], _ptr(q_len), scale, ctypes.byref(score), n_split,
+                                out.data_ptr(), codes[out.dtype], lse.data_ptr(), workspace.data_ptr(),
+                                workspace.numel(), _stream(stream)))
 
 
 def tree_accept(cache: PackedCache, seq_len, n_q: int, path, path_len, new_len, q_len=None, flag=None, stream=None):
@@ -467,13 +485,17 @@ def tree_accept(cache: PackedCache, seq_len, n_q: int, path, path_len, new_len, 
     the front of its drafted positions, bit for bit, and store the new lengths in new_len (int32 [batch], not
     seq_len itself). flag: int32 [1], set to 2 by an entry out of range."""
     import torch
-    B = cache.batch
-    for t, what in ((seq_len, "seq_len"), (path_len, "path_len"), (new_len, "new_len"), (q_len, "q_len")):
-        _expect(t, what, (B,), torch.int32)
-    _expect(path, "path", (B, path.shape[-1]), torch.int32)
-    _expect(flag, "flag", (1,), torch.int32)
-    _check(load().ckv_tree_accept(cache.ref(), _ptr(seq_len), n_q, _ptr(q_len), _ptr(path), path.shape[-1],
-                                  _ptr(path_len), _ptr(new_len), _ptr(flag), _stream(stream)))
+    dev, i32, rows = _cache_device(cache), (torch.int32,), (cache.batch,)
+    _expect(seq_len, "seq_len", rows, i32, dev)
+    _expect(path_len, "path_len", rows, i32, dev)
+    _expect(new_len, "new_len", rows, i32, dev)
+    _expect(path, "path", rows + path.shape[1:2], i32, dev)
+    if q_len is not None:
+        _expect(q_len, "q_len", rows, i32, dev)
+    if flag is not None:
+        _expect(flag, "flag", (1,), i32, dev)
+    _check(load().ckv_tree_accept(cache.ref(), seq_len.data_ptr(), n_q, _ptr(q_len), path.data_ptr(), path.shape[1],
+                                  path_len.data_ptr(), new_len.data_ptr(), _ptr(flag), _stream(stream)))
 
 
 def selftest_bounded_waits(workspace, stream=None):
