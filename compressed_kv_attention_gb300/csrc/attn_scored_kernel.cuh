@@ -1,6 +1,8 @@
 // attn_scored_kernel.cuh — attn_scored and attn_tree with few query rows, on
 // mma.sync: the split-K decode over the packed records with scored.cuh's masks
-// and logits, one row group (8 query rows of one kv head) per CTA.
+// and logits, one row group (8 query rows of one kv head) per CTA. Every tile
+// group (a warp, or two at D = 512) streams its own records through its own
+// stages, so no warp waits for another but its partner.
 //
 // Mathematics: the decode kernel's (S^T = K_hat Q^T and O^T += C^T P'^T, the
 // codes widened in registers, one online softmax over the row's keys), with
@@ -20,20 +22,22 @@ struct CScored : DecodeShape<D> {
   using Sh = DecodeShape<D>;
   static constexpr int NGRP = ROT ? D / kRotGroup : 1;
   static constexpr int REC = record_bytes(D, B, NGRP);
-  static constexpr int STAGE = Sh::NP * REC;
-  static constexpr int NSTAGE = 4;
-  static constexpr int THREADS = (Sh::NCW + 1) * 32;
+  static constexpr int NSTAGE = 4;  // records in flight per tile group
+  static constexpr int THREADS = Sh::NCW * 32;
   // The rotated tiers round V's fragments to fp16 once more (the group norms
   // scale them), so their P' is always the fp16 pair.
   static constexpr bool PSPLIT = ROT || D <= 128;
   static constexpr int LUT = CDec<D, B, ROT>::LUT;
   static constexpr int RED_BYTES = Sh::NP * Sh::RED_FLOATS * 4;
-  static constexpr int RING = (NSTAGE * STAGE > RED_BYTES) ? NSTAGE * STAGE : RED_BYTES;
+  static constexpr int RING = (Sh::NP * NSTAGE * REC > RED_BYTES) ? Sh::NP * NSTAGE * REC : RED_BYTES;
   static constexpr int OFF_XCHG = (RING + 127) / 128 * 128;
   static constexpr int OFF_ML = OFF_XCHG + Sh::XCHG_BYTES;
   static constexpr int OFF_QB = OFF_ML + Sh::NP * 16 * 4;
   static constexpr int OFF_BAR = OFF_QB + Sh::NCW * Sh::NB_W * 4 * 2 * 4;
-  static constexpr int SMEM = OFF_BAR + 2 * NSTAGE * 8 + 16;
+  static constexpr int SMEM = OFF_BAR + Sh::NP * NSTAGE * 8 + 16;
+  // Up to head dim 128 the accumulators leave the registers for a second CTA on the SM.
+  static constexpr int PER_SM = D <= 128 ? 2 : 1;
+  static_assert(PER_SM * (SMEM + LUT * 128 + 4096) <= 227 * 1024, "shared memory");
 };
 
 // load_q_frags for bf16 queries, converted to fp16 (exact within fp16's range).
@@ -51,7 +55,8 @@ __device__ __forceinline__ void convert_q_frags(uint32_t (&qf)[NBW][4]) {
 }  // namespace
 
 template <int D, int B, int ROT>
-__global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, 1) attn_scored_kernel(ScoredArgs a) {
+__global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, CScored<D, B, ROT>::PER_SM)
+    attn_scored_kernel(ScoredArgs a) {
   using C = CScored<D, B, ROT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) uint32_t s_lut[C::LUT * 32];
@@ -65,24 +70,21 @@ __global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, 1) attn_scored_ke
   const int group_q = a.n_q_heads / a.n_kv_heads;
   const int R = group_q * a.n_q;
 
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* empty = full + C::NSTAGE;
+  const int group = warp / C::WT, wh = warp % C::WT;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + group * C::NSTAGE;
   float4* xbuf = reinterpret_cast<float4*>(smem + C::OFF_XCHG);
   float* mlbuf = reinterpret_cast<float*>(smem + C::OFF_ML);
 
   // Before the previous grid on the stream has finished: barriers and table.
-  if (warp == C::NCW) {
-    if (lane == 0) {
-      for (int s = 0; s < C::NSTAGE; ++s) {
-        mbar_init(&full[s], 1);
-        mbar_init(&empty[s], C::NCW);
-      }
-      s_abort = 0;
-      fence_barrier_init();
-    }
-  } else {
+  if (threadIdx.x == 0) {
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    for (int s = 0; s < C::NP * C::NSTAGE; ++s) mbar_init(&bars[s], 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  {
     constexpr float inv = 1.0f / centroid_scale(B);
-    for (int e = threadIdx.x; e < C::LUT * 32; e += C::NCW * 32) {
+    for (int e = threadIdx.x; e < C::LUT * 32; e += C::THREADS) {
       const int f = e >> 5;
       const int klo = (B == 4) ? f : (f & ((1 << B) - 1));
       const int khi = (B == 4) ? f : (f >> B);
@@ -96,15 +98,14 @@ __global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, 1) attn_scored_ke
   scored_lengths(a, b, threadIdx.x == 0, seqlen, n);
   const int base = seqlen - n;
   if (threadIdx.x < 8) s_row[threadIdx.x] = scored_row(a, b, kvh, rg * 8 + threadIdx.x, seqlen, n);
-  if (warp >= 2) scored_depths(a, b, n, threadIdx.x - 64, s_depth);
+  if (warp >= 2 && warp < 4) scored_depths(a, b, n, threadIdx.x - 64, s_depth);
   uint32_t qf[C::NB_W][4];
-  if (warp < C::NCW) {
+  {
     const int rr = rg * 8 + (lane >> 2);
     int qi = 0, h = 0;
     const bool ok = rr < R;
     if (ok) row_to_query(rr, group_q, kvh, qi, h);
-    load_q_frags<C::NB_W>(qf, a.q + ((int64_t)(b * a.n_q + qi) * a.n_q_heads + h) * D, ok,
-                          (warp % C::WT) * C::NB_W, lane & 3);
+    load_q_frags<C::NB_W>(qf, a.q + ((int64_t)(b * a.n_q + qi) * a.n_q_heads + h) * D, ok, wh * C::NB_W, lane & 3);
     if (a.q_bf16) convert_q_frags<C::NB_W>(qf);
   }
   __syncthreads();
@@ -125,39 +126,20 @@ __global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, 1) attn_scored_ke
   const int64_t lo_t = ghi > glo ? glo / kTile : 0, hi_t = ghi > glo ? (ghi + kTile - 1) / kTile : 0;
   const int64_t tb = lo_t + (int64_t)split * (hi_t - lo_t) / a.n_split;
   const int64_t te = lo_t + (int64_t)(split + 1) * (hi_t - lo_t) / a.n_split;
-  const int n_iters = static_cast<int>((te - tb + C::NP - 1) / C::NP);
+  // This group's tiles: tb + group, + NP, ... below te, each one record, one
+  // bulk copy and one stage of the group's own ring.
+  const int n_iters = te > tb + group ? static_cast<int>((te - tb - group + C::NP - 1) / C::NP) : 0;
   const uint8_t* gbase = a.cache + (int64_t)(b * a.n_kv_heads + kvh) * (a.capacity / kTile) * C::REC;
+  uint8_t* const gring = smem + group * C::NSTAGE * C::REC;
+  auto issue = [&](int it) {  // one lane of the group
+    const int s = it % C::NSTAGE;
+    mbar_arrive_expect_tx(&full[s], C::REC);
+    bulk_g2s(gring + s * C::REC, gbase + (tb + group + (int64_t)it * C::NP) * C::REC, C::REC, &full[s]);
+  };
+  const bool leader = wh == 0 && lane == 0;
+  if (leader)
+    for (int it = 0; it < n_iters && it < C::NSTAGE; ++it) issue(it);
 
-  if (warp == C::NCW) {
-    // ------------------------------------------------------------ producer --
-    if (lane == 0) {
-      int issued = 0;
-      for (int it = 0; it < n_iters; ++it) {
-        const int s = it % C::NSTAGE;
-        if (it >= C::NSTAGE && !mbar_wait(&empty[s], ((it / C::NSTAGE) - 1) & 1)) {
-          *(volatile int*)&s_abort = 1;
-          raise_flag(a.flag, kFlagWaitTimeout);
-        }
-        if (*(volatile int*)&s_abort) break;
-        const int64_t first = tb + (int64_t)it * C::NP;
-        const uint32_t cnt = te - first < C::NP ? (uint32_t)(te - first) : (uint32_t)C::NP;
-        mbar_arrive_expect_tx(&full[s], cnt * C::REC);
-        bulk_g2s(smem + s * C::STAGE, gbase + first * C::REC, cnt * C::REC, &full[s]);
-        ++issued;
-      }
-      // Do not leave while a copy may still be landing in this CTA's memory.
-      for (int k = issued > C::NSTAGE ? issued - C::NSTAGE : 0; k < issued; ++k) {
-        if (!mbar_wait(&full[k % C::NSTAGE], (k / C::NSTAGE) & 1)) {
-          raise_flag(a.flag, kFlagWaitTimeout);
-          break;
-        }
-      }
-    }
-    return;
-  }
-
-  // -------------------------------------------------------------- consumers --
-  const int group = warp / C::WT, wh = warp % C::WT;
   const int g = lane >> 2, t = lane & 3;
   float* qb_warp = reinterpret_cast<float*>(smem + C::OFF_QB) + warp * C::NB_W * 8;
   q_block_bias<C::NB_W>(qf, lane, qb_warp);
@@ -171,25 +153,39 @@ __global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, 1) attn_scored_ke
   for (int i = 0; i < C::MT_W; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
   SoftmaxState st{-INFINITY, -INFINITY, 0.0f, 0.0f};
 
-  const uint32_t ring = smem_u32(smem);
+  const uint32_t ring = smem_u32(gring);
   const uint8_t* lut_bytes = reinterpret_cast<const uint8_t*>(s_lut);
   const uint32_t lane4 = (uint32_t)lane << 2;
 
-  for (int it = 0; it < n_iters; ++it) {
+  auto wait_stage = [&](int it) {
     if (!*(volatile int*)&s_abort) {
       if (!mbar_wait(&full[it % C::NSTAGE], (it / C::NSTAGE) & 1)) {
         *(volatile int*)&s_abort = 1;
         raise_flag(a.flag, kFlagWaitTimeout);
       }
     }
+  };
+  auto record = [&](int it) { return ring + (it % C::NSTAGE) * C::REC; };
+  // S of the next tile is in flight under the softmax and P.V of this one (two
+  // warps to a tile: each one's half crosses through shared memory).
+  float S[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (n_iters > 0) {
+    wait_stage(0);
+    qk_tile<D>(record(0), wh, lane, qf, qb, S);
+    if constexpr (C::WT == 2) exchange_S<2>(S, xbuf, group, wh, 0, lane);
+  }
+  for (int it = 0; it < n_iters; ++it) {
     const int64_t tile = tb + (int64_t)it * C::NP + group;
-    if (tile < te) {
-      const uint32_t rb = ring + (it % C::NSTAGE) * C::STAGE + group * C::REC;
+    const bool next = it + 1 < n_iters;
+    float Sn[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (next) {
+      wait_stage(it + 1);
+      qk_tile<D>(record(it + 1), wh, lane, qf, qb, Sn);
+      if constexpr (C::WT == 2) xchg_put<2>(Sn, xbuf, group, wh, (it + 1) & 1, lane);
+    }
+    {
+      const uint32_t rb = record(it);
       const int64_t tpos = tile * kTile;
-      float S[4];
-      qk_tile<D>(rb, wh, lane, qf, qb, S);
-      if constexpr (C::WT == 2) exchange_S<2>(S, xbuf, group, wh, it & 1, lane);
-
       // Visibility: position tpos + g is bit g of its row's word, tpos + g + 8 bit g + 8.
       uint32_t v0 = 0xffffu, v1 = 0xffffu, any = 0xffffu;
       if (tpos < flo || tpos + kTile > fhi) {
@@ -261,8 +257,15 @@ __global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, 1) attn_scored_ke
       }
       pv_tile<D, B, ROT, C::PSPLIT>(rb, lut_bytes, lane4, wh, lane, movmatrix_trans(X0), movmatrix_trans(X1), pl, acc, nA, nB);
     }
+    // The record is read: its stage takes the tile NSTAGE further (at two warps
+    // per tile past the barrier of the exchange).
     __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[it % C::NSTAGE]);
+    if constexpr (C::WT == 2) {
+      if (next) xchg_get<2>(Sn, xbuf, group, (it + 1) & 1, lane);
+    }
+    if (leader && it + C::NSTAGE < n_iters) issue(it + C::NSTAGE);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[e] = Sn[e];
   }
 
   // Rows that see nothing took part in the tiles that every other row sees

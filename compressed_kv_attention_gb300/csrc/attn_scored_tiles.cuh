@@ -14,15 +14,19 @@
 //               running maximum moves only when it grows by 2^2 or more (O in
 //               TMEM is rescaled then; P' stays below 4 norms, fp16 for any
 //               norm up to a quarter of its range)
-//   warps 8-15  widening: codes from global memory (fetched two chunks ahead)
-//               to fp16 operands in a ring of shared-memory slots, each 128
-//               dims of the step's K (hi, then lo) or V
+//   warps 8-15  widening: codes from global memory to fp16 operands in a ring
+//               of shared-memory slots, each 128 dims of the step's K (hi, then
+//               lo) or V. Two teams of four warps fill different slots at once
+//               (even and odd chunks; up to head dim 128 one K and one V), since
+//               a slot's time is mostly latency: the wait for the slot, the
+//               table lookups, the proxy fence. Each fetches the codes of its
+//               next chunk as it consumes the current one's.
 //   warp 16     issues the MMAs as slots fill; a slot is free again when its
 //               MMAs have completed
-// S is double-buffered up to head dim 256, so that S of the next step runs
-// under the softmax of this one. At D = 512 the 512 TMEM columns hold S (64)
-// and 448 output dims; the last 64 dims of P' C go through S's columns once the
-// softmax has read them and are summed in the softmax threads' registers.
+// S is double-buffered, so that S of the next step runs under the softmax of
+// this one. At D = 512 the 512 TMEM columns hold the two S (128) and 384 output
+// dims; the last 128 dims of P' C go through the S columns that the softmax has
+// just read, 64 at a time, and are summed in the softmax threads' registers.
 // The 128-byte-swizzle K-major layout holds every operand.
 #pragma once
 
@@ -41,10 +45,11 @@ struct CTiles {
   static constexpr int REC = record_bytes(D, B, NGRP);
   static constexpr int CW = D < 128 ? D : 128;      // dims per slot
   static constexpr int NCH = D / CW;                // slots per step of each operand
-  static constexpr int OT = D < 448 ? D : 448;      // output dims in TMEM
+  static constexpr int OT = D < 384 ? D : 384;      // output dims in TMEM
   static constexpr int OR = D - OT;                 // output dims in registers
-  static constexpr int NS = D == 512 ? 1 : 2;       // S buffers
+  static constexpr int NS = 2;                      // S buffers
   static constexpr int OCOL = 64 * NS;              // first O column
+  static_assert(OR == 0 || OR == CW, "the tail is one slot of V");
   static constexpr bool PSPLIT = ROT || D <= 128;
   static constexpr int LUT = B == 3 ? 64 : 16;
   static constexpr int SLOT = NKV * CW * 2;
@@ -52,22 +57,23 @@ struct CTiles {
   static constexpr int Q_OFF = 0;
   static constexpr int P_OFF = M * D * 2;
   static constexpr int RING_OFF = P_OFF + (PSPLIT ? 2 : 1) * P_BYTES;
-  static constexpr int TAIL = LUT * 128 + 2 * NKV * 4 + 4 * M * 4 + M * static_cast<int>(sizeof(RowInfo));
+  static constexpr int TAIL = LUT * 128 + 8 * NKV * 4 + 4 * M * 4 + M * static_cast<int>(sizeof(RowInfo));
   static constexpr int BUDGET = 227 * 1024 - 1024 - 1024;  // alignment, static shared memory
   static constexpr int NSLOT_FIT = (BUDGET - RING_OFF - TAIL) / SLOT;
   static constexpr int NSLOT = NSLOT_FIT > 8 ? 8 : NSLOT_FIT;
   static_assert(NSLOT >= 3, "a K chunk takes two slots");
   static constexpr int LUT_OFF = RING_OFF + NSLOT * SLOT;
   static constexpr int NORM_OFF = LUT_OFF + LUT * 128;
-  static constexpr int MAX_OFF = NORM_OFF + 2 * NKV * 4;  // [2][2][M]: the halves' row maxima, later sums
+  static constexpr int MAX_OFF = NORM_OFF + 8 * NKV * 4;  // norms [4][2][NKV]; [2][2][M]: the halves' row maxima, later sums
   static constexpr int ROW_OFF = MAX_OFF + 4 * M * 4;
   static constexpr int BYTES = ROW_OFF + M * static_cast<int>(sizeof(RowInfo));
   // At least half the SM's shared memory: one CTA, and its 512 TMEM columns, per SM.
   static constexpr int SMEM = (BYTES + 1024 > 120 * 1024 ? BYTES + 1024 : 120 * 1024);
   static constexpr int SOFT = 256, WIDEN = 256;     // threads of the softmax and widening roles
+  static constexpr int TEAM = WIDEN / 2;
   static constexpr int THREADS = SOFT + WIDEN + 128;  // the MMA warp, in a warpgroup of its own
   // Registers per thread of the roles: 5 warpgroups are launched with 96 each.
-  static constexpr int REG_SOFT = 136, REG_WIDEN = 88, REG_MMA = 32;
+  static constexpr int REG_SOFT = D == 512 ? 152 : 136, REG_WIDEN = D == 512 ? 72 : 88, REG_MMA = 32;
   static_assert(2 * REG_SOFT + 2 * REG_WIDEN + REG_MMA <= 5 * 96, "the roles share the launch's registers");
   // Output staging of the epilogue: RP rows at a time, padded by 16 bytes.
   static constexpr int STRIDE = D + 4;
@@ -100,7 +106,8 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
   constexpr int M = C::M, NKV = C::NKV, CW = C::CW, NCH = C::NCH, NS = C::NS, NSLOT = C::NSLOT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint32_t s_tmem;
-  __shared__ __align__(8) uint64_t b_full[8], b_free[8], b_sfull[2], b_sfree[2], b_pfull, b_pvdone, b_tail;
+  __shared__ __align__(8) uint64_t b_full[8], b_free[8], b_sfull[2], b_sfree[2], b_pfull, b_pvdone, b_tail,
+      b_tread;
   __shared__ int s_abort, s_red[4][4];
   __shared__ int8_t s_depth[64];
 
@@ -123,20 +130,22 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
   const int b = bh / a.n_kv_heads, kvh = bh % a.n_kv_heads;
   const int q0 = qt * QT;
   const int rows = min(QT, a.n_q - q0) * G;  // real rows of the tile
+  const int act = (rows + 31) / 32;          // 32-row groups with a real row: the others' softmax warps only store
 
   if (warp == 0) tmem_alloc(&s_tmem, 512);
   if (tid == 32) {
     for (int s = 0; s < NSLOT; ++s) {
-      mbar_init(&b_full[s], C::WIDEN / 32);
+      mbar_init(&b_full[s], C::TEAM / 32);
       mbar_init(&b_free[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&b_sfull[s], 1);
-      mbar_init(&b_sfree[s], C::SOFT / 32);
+      mbar_init(&b_sfree[s], 2 * act);
     }
-    mbar_init(&b_pfull, C::SOFT / 32);
+    mbar_init(&b_pfull, 2 * act);
     mbar_init(&b_pvdone, 1);
     mbar_init(&b_tail, 1);
+    mbar_init(&b_tread, 2 * act);
     s_abort = 0;
     fence_barrier_init();
   }
@@ -187,6 +196,11 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     }
     *reinterpret_cast<uint4*>(sQ + sw128_offset(r, k0, M)) = v;
   }
+  // P' of the row groups without a real row stays zero.
+  for (int e = act * 32 * 8 + tid; e < M * 8; e += C::THREADS) {
+    reinterpret_cast<uint4*>(sP)[e] = make_uint4(0, 0, 0, 0);
+    if constexpr (C::PSPLIT) reinterpret_cast<uint4*>(sP + C::P_BYTES)[e] = make_uint4(0, 0, 0, 0);
+  }
   fence_proxy_async();
   tc_fence_before();
   __syncthreads();
@@ -208,6 +222,7 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
 
   // A wait that runs out raises the flag; every later wait is skipped, so that all roles finish.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity & 1u)) return;
     if (!*(volatile int*)&s_abort && !mbar_wait(bar, parity & 1u)) {
       *(volatile int*)&s_abort = 1;
       raise_flag(a.flag, kFlagWaitTimeout);
@@ -217,61 +232,55 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
   if (tid >= C::SOFT && tid < C::SOFT + C::WIDEN) {
     // ------------------------------------------------------------ widening --
     regs_dec<C::REG_WIDEN>();
-    const int wt = tid - C::SOFT;  // 0 .. 255
-    int slot = 0;                  // the next slot to fill, and the parity of its last release
-    uint32_t turn = 1;             // (a slot's first use waits for the phase before its first: it passes at once)
-    auto slot_done = [&]() {
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b_full[slot]);
-      if (++slot == NSLOT) slot = 0, turn ^= 1u;
+    const int team = (tid - C::SOFT) / C::TEAM, tw = (tid - C::SOFT) % C::TEAM;
+    // The slots' order: K of step 0, then for every step i K of step i + 1 (all
+    // but the last) and V of step i; hi and lo of a chunk are neighbours.
+    auto k_index = [&](int step, int c) { return (step == 0 ? 0 : 3 * NCH * step - NCH) + 2 * c; };
+    auto v_index = [&](int step, int c) { return 3 * NCH * step + (step + 1 < n_steps ? 4 : 2) * NCH + c; };
+    auto slot_wait = [&](int g) {  // a slot's first use waits for the phase before its first, which passes at once
+      wait(&b_free[g % NSLOT], g / NSLOT + 1);
+    };
+    auto slot_done = [&](int g) {
+      if (lane == 0) mbar_arrive(&b_full[g % NSLOT]);
     };
     // K chunk c of a step: 4 records x CW / 32 blocks x 32 lanes of 16 bytes,
     // each 8 dims of tokens kpp and kpp + 8 of a record.
-    constexpr int PIECES = 4 * (CW / 32) * 32, KR = PIECES / C::WIDEN;
-    static_assert(KR >= 1 && PIECES % C::WIDEN == 0, "K pieces per thread");
+    constexpr int PIECES = 4 * (CW / 32) * 32, KR = PIECES / C::TEAM;
+    static_assert(KR >= 1 && PIECES % C::TEAM == 0, "K pieces per thread");
     const int kq = lane >> 3, kpp = lane & 7;
-    // Codes are fetched two chunks ahead (one, of a whole step, where a step has one chunk).
-    constexpr int AHEAD = NCH > 1 ? 2 : 1;
-    uint4 kw_[AHEAD][KR];
-    uint32_t ks_[AHEAD][KR];  // the two tokens' scales
-    auto fetch_k = [&](int step, int c, uint4 (&kw)[KR], uint32_t (&ks)[KR]) {
-      if (step >= n_steps) return;
-#pragma unroll
-      for (int r = 0; r < KR; ++r) {
-        const int u = r * 8 + (wt >> 5);  // (record, block) of this warp
-        const int64_t rec = (int64_t)(s0 + step) * 4 + u / (CW / 32);
-        const int blk = c * (CW / 32) + u % (CW / 32);
-        if (rec < n_rec) {
-          const uint8_t* p = stream + rec * C::REC;
-          kw[r] = *reinterpret_cast<const uint4*>(p + (blk * 32 + 4 * kpp + kq) * 16);
-          const uint16_t* sc = reinterpret_cast<const uint16_t*>(p + k_scale_offset(D)) + blk;
-          ks[r] = sc[kpp * C::NB] | (uint32_t)sc[(kpp + 8) * C::NB] << 16;
-        } else {
-          kw[r] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-          ks[r] = 0u;
-        }
+    uint4 kw[KR];
+    uint32_t ks[KR];  // the two tokens' scales
+    auto fetch_k = [&](int step, int c, int r) {
+      const int u = r * (C::TEAM / 32) + (tw >> 5);  // (record, block) of this warp
+      const int64_t rec = (int64_t)(s0 + step) * 4 + u / (CW / 32);
+      const int blk = c * (CW / 32) + u % (CW / 32);
+      if (step < n_steps && rec < n_rec) {
+        const uint8_t* p = stream + rec * C::REC;
+        kw[r] = *reinterpret_cast<const uint4*>(p + (blk * 32 + 4 * kpp + kq) * 16);
+        const uint16_t* sc = reinterpret_cast<const uint16_t*>(p + k_scale_offset(D)) + blk;
+        ks[r] = sc[kpp * C::NB] | (uint32_t)sc[(kpp + 8) * C::NB] << 16;
+      } else {
+        kw[r] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+        ks[r] = 0u;
       }
     };
-    auto widen_k = [&](int step, int c, uint4 (&kw)[KR], uint32_t (&ks)[KR]) {
-      uint4 w4[KR];
-      uint32_t sc[KR];
-#pragma unroll
-      for (int r = 0; r < KR; ++r) w4[r] = kw[r], sc[r] = ks[r];
-      if (c + AHEAD < NCH) fetch_k(step, c + AHEAD, kw, ks);
-      else fetch_k(step + 1, c + AHEAD - NCH, kw, ks);
-      // hi is handed over before lo is stored.
-      uint4 lo4[KR][2];
-      wait(&b_free[slot], turn);
-      uint8_t* dst = ring + slot * C::SLOT;
+    // Widens the fetched chunk c of `step` and fetches (step_n, c_n).
+    auto widen_k = [&](int step, int c, int step_n, int c_n) {
+      const int g = k_index(step, c);
+      slot_wait(g);
+      slot_wait(g + 1);
+      uint8_t* const s_hi = ring + g % NSLOT * C::SLOT;
+      uint8_t* const s_lo = ring + (g + 1) % NSLOT * C::SLOT;
 #pragma unroll
       for (int r = 0; r < KR; ++r) {
-        const int u = r * 8 + (wt >> 5);
+        const int u = r * (C::TEAM / 32) + (tw >> 5);
         const int row0 = u / (CW / 32) * kTile + kpp, k0 = (u % (CW / 32)) * 32 + 8 * kq;
-        const uint32_t w[4] = {w4[r].x, w4[r].y, w4[r].z, w4[r].w};
+        const uint32_t w[4] = {kw[r].x, kw[r].y, kw[r].z, kw[r].w};
+        const uint32_t sc = ks[r];
+        fetch_k(step_n, c_n, r);
 #pragma unroll
         for (int hs = 0; hs < 2; ++hs) {
-          const uint32_t dd = __byte_perm(sc[r], 0u, hs ? 0x3232 : 0x1010);
+          const uint32_t dd = __byte_perm(sc, 0u, hs ? 0x3232 : 0x1010);
           const __half2 d2 = *reinterpret_cast<const __half2*>(&dd);
           uint32_t qh[4], hi[4], lo[4];
           i8x4_to_half2x2(w[2 * hs], qh[0], qh[1]);
@@ -284,61 +293,47 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
             hi[e] = *reinterpret_cast<const uint32_t*>(&h);
             lo[e] = *reinterpret_cast<const uint32_t*>(&l);
           }
-          *reinterpret_cast<uint4*>(dst + sw128_offset(row0 + 8 * hs, k0, NKV)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          lo4[r][hs] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          const uint32_t off = sw128_offset(row0 + 8 * hs, k0, NKV);
+          *reinterpret_cast<uint4*>(s_hi + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(s_lo + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
-      slot_done();
-      wait(&b_free[slot], turn);
-      dst = ring + slot * C::SLOT;
-#pragma unroll
-      for (int r = 0; r < KR; ++r) {
-        const int u = r * 8 + (wt >> 5);
-        const int row0 = u / (CW / 32) * kTile + kpp, k0 = (u % (CW / 32)) * 32 + 8 * kq;
-#pragma unroll
-        for (int hs = 0; hs < 2; ++hs)
-          *reinterpret_cast<uint4*>(dst + sw128_offset(row0 + 8 * hs, k0, NKV)) = lo4[r][hs];
-      }
-      slot_done();
+      fence_proxy_async();
+      __syncwarp();
+      slot_done(g);
+      slot_done(g + 1);
     };
     // V chunk c of a step: units of (lane stream, 8 dims), 16 fields of 2B
-    // bits in B words of the stream. Unit v = 16 (...) + 4 record + (stream % 4).
+    // bits in B words of the stream. Unit v = 16 part + 4 record + (stream % 4).
     constexpr int GDIM = D / 8;                             // dims per lane stream
-    constexpr int SUB = GDIM / 8 > 0 ? GDIM / 8 : 1;        // 8-dim parts of a stream
-    constexpr int UNITS = 16 * (CW / 8), VR = (UNITS + C::WIDEN - 1) / C::WIDEN;
-    static_assert(VR == 1, "one V unit per thread and chunk");
-    const bool v_on = wt < UNITS;
-    const int v_rec = (wt >> 2) & 3, v_t = wt & 3, v_part = wt >> 4;  // 8-dim part of the chunk
+    constexpr int SUB = GDIM / 8;                           // 8-dim parts of a stream
+    constexpr int VR = 16 * (CW / 8) / C::TEAM;             // units per thread and chunk
+    static_assert(VR >= 1, "V units per thread");
+    const int v_rec = (tw >> 2) & 3, v_t = tw & 3;
     constexpr int GR = v_granule(D, B);
-    uint32_t vw_[AHEAD][B], vn_[AHEAD][2];
-    auto v_chunk = [&](int k) { return C::OR > 0 ? (k + NCH - 1) % NCH : k; };  // D = 512: the tail's chunk first
-    auto fetch_v = [&](int step, int k, uint32_t (&vw)[B], uint32_t (&vn)[2]) {
-      if (step >= n_steps || !v_on) return;
-      const int part = v_chunk(k) * (CW / 8) + v_part;  // dims 8 part .. 8 part + 7
+    uint32_t vw[VR][B], vn[VR][2];
+    auto fetch_v = [&](int step, int c, int r) {
+      const int part = c * (CW / 8) + (tw >> 4) + r * (C::TEAM / 16);  // dims 8 part .. 8 part + 7
       const int L = 4 * (part / SUB) + v_t, w0 = (part % SUB) * B;
       const int64_t rec = (int64_t)(s0 + step) * 4 + v_rec;
+      const bool in = step < n_steps && rec < n_rec;
       const uint8_t* p = stream + rec * C::REC;
 #pragma unroll
       for (int w = 0; w < B; ++w) {
         const int sb = 4 * (w0 + w);
-        vw[w] = rec < n_rec ? *reinterpret_cast<const uint32_t*>(p + v_code_offset(D) + ((sb / GR) * 32 + L) * GR + sb % GR)
-                            : 0u;
+        vw[r][w] = in ? *reinterpret_cast<const uint32_t*>(p + v_code_offset(D) + ((sb / GR) * 32 + L) * GR + sb % GR) : 0u;
       }
       if constexpr (ROT) {  // the norms of positions 2t, 2t + 1 and 2t + 8, 2t + 9
         const uint8_t* nb = p + v_norm_offset(D, B) + 2 * (kTile * (8 * part / kRotGroup) + 2 * v_t);
-        vn[0] = rec < n_rec ? *reinterpret_cast<const uint32_t*>(nb) : 0u;
-        vn[1] = rec < n_rec ? *reinterpret_cast<const uint32_t*>(nb + 16) : 0u;
+        vn[r][0] = in ? *reinterpret_cast<const uint32_t*>(nb) : 0u;
+        vn[r][1] = in ? *reinterpret_cast<const uint32_t*>(nb + 16) : 0u;
       }
     };
-    auto widen_v = [&](int step, int k, uint32_t (&vw)[B], uint32_t (&vn)[2]) {
-      uint32_t w[B], nn[2] = {ROT ? vn[0] : 0u, ROT ? vn[1] : 0u};
-#pragma unroll
-      for (int e = 0; e < B; ++e) w[e] = vw[e];
-      if (k + AHEAD < NCH) fetch_v(step, k + AHEAD, vw, vn);
-      else fetch_v(step + 1, k + AHEAD - NCH, vw, vn);
+    auto widen_v = [&](int step, int c, int step_n, int c_n) {
+      uint32_t keep[2] = {~0u, ~0u};  // norms of positions that no row sees may hold any bytes
       if constexpr (ROT) {
         const int pos0 = (s0 + step) * NKV;
-        if (pos0 < flo || pos0 + NKV > fhi) {  // norms of positions that no row sees may hold any bytes
+        if (pos0 < flo || pos0 + NKV > fhi) {
           uint32_t any = 0u;
           for (int rec = 0; rec < 4; ++rec) {
             uint32_t m = 0u;
@@ -347,15 +342,22 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
             if (rec == v_rec) any = m;
           }
           const uint32_t ma = any >> (2 * v_t), mb = any >> (2 * v_t + 8);
-          nn[0] &= (ma & 1u ? 0xffffu : 0u) | (ma & 2u ? 0xffff0000u : 0u);
-          nn[1] &= (mb & 1u ? 0xffffu : 0u) | (mb & 2u ? 0xffff0000u : 0u);
+          keep[0] = (ma & 1u ? 0xffffu : 0u) | (ma & 2u ? 0xffff0000u : 0u);
+          keep[1] = (mb & 1u ? 0xffffu : 0u) | (mb & 2u ? 0xffff0000u : 0u);
         }
       }
-      wait(&b_free[slot], turn);
-      uint8_t* const dst = ring + slot * C::SLOT;
-      if (v_on) {
-        const uint32_t lut = smem_u32(sLut) + (uint32_t)(lane << 2);
-        const int tok = v_rec * kTile + 2 * v_t;
+      const int g = v_index(step, c);
+      slot_wait(g);
+      uint8_t* const dst = ring + g % NSLOT * C::SLOT;
+      const uint32_t lut = smem_u32(sLut) + (uint32_t)(lane << 2);
+      const int tok = v_rec * kTile + 2 * v_t;
+#pragma unroll
+      for (int r = 0; r < VR; ++r) {
+        const int v_part = (tw >> 4) + r * (C::TEAM / 16);  // 8-dim part of the chunk
+        uint32_t w[B], nn[2] = {ROT ? vn[r][0] & keep[0] : 0u, ROT ? vn[r][1] & keep[1] : 0u};
+#pragma unroll
+        for (int e = 0; e < B; ++e) w[e] = vw[r][e];
+        fetch_v(step_n, c_n, r);
         auto field = [&](int f) {  // dim 2 (f / 4) + (f & 1), positions + 8 (f >> 1 & 1)
           uint32_t val;
           if constexpr (B == 3) {
@@ -375,32 +377,52 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
         // A warp holds two parts, whose rows share their banks: one writes the
         // upper eight positions of a record while the other writes the lower.
         const bool flip = v_part & 1;
+        // Eight lookups in flight, then their stores.
 #pragma unroll
-        for (int f = 0; f < 16; ++f) {
-          if (f & 2) continue;
-          const uint32_t lo = field(f), hi = field(f | 2);
-          const int dim = v_part * 8 + 2 * (f >> 2) + (f & 1);
-          *reinterpret_cast<uint32_t*>(dst + sw128_offset(dim, tok + (flip ? 8 : 0), CW)) = flip ? hi : lo;
-          *reinterpret_cast<uint32_t*>(dst + sw128_offset(dim, tok + (flip ? 0 : 8), CW)) = flip ? lo : hi;
+        for (int f0 = 0; f0 < 16; f0 += 8) {
+          uint32_t val[8];
+#pragma unroll
+          for (int f = 0; f < 8; ++f) val[f] = field(f0 + f);
+#pragma unroll
+          for (int f = 0; f < 8; ++f) {
+            const int dim = v_part * 8 + 2 * ((f0 + f) >> 2) + (f & 1), h = f >> 1 & 1;
+            *reinterpret_cast<uint32_t*>(dst + sw128_offset(dim, tok + 8 * (flip ? 1 - h : h), CW)) =
+                flip ? val[f ^ 2] : val[f];
+          }
         }
       }
-      slot_done();
+      fence_proxy_async();
+      __syncwarp();
+      slot_done(g);
     };
+    if constexpr (NCH == 1) {
+      if (team == 0) {
 #pragma unroll
-    for (int c = 0; c < AHEAD; ++c) {
-      fetch_k(0, c, kw_[c], ks_[c]);
-      fetch_v(0, c, vw_[c], vn_[c]);
-    }
-    auto all_k = [&](int step) {
+        for (int r = 0; r < KR; ++r) fetch_k(0, 0, r);
+        for (int i = 0; i < n_steps; ++i) widen_k(i, 0, i + 1, 0);
+      } else {
 #pragma unroll
-      for (int c = 0; c < NCH; ++c) widen_k(step, c, kw_[c % AHEAD], ks_[c % AHEAD]);
-    };
-    if (NS == 2 && n_steps > 0) all_k(0);
-    for (int i = 0; i < n_steps; ++i) {
-      if constexpr (NS == 1) all_k(i);
-      else if (i + 1 < n_steps) all_k(i + 1);
+        for (int r = 0; r < VR; ++r) fetch_v(0, 0, r);
+        for (int i = 0; i < n_steps; ++i) widen_v(i, 0, i + 1, 0);
+      }
+    } else {
+      constexpr int PER = NCH / 2;  // chunks of a step per team: team, team + 2, ...
 #pragma unroll
-      for (int k = 0; k < NCH; ++k) widen_v(i, k, vw_[k % AHEAD], vn_[k % AHEAD]);
+      for (int r = 0; r < KR; ++r) fetch_k(0, team, r);
+#pragma unroll
+      for (int r = 0; r < VR; ++r) fetch_v(0, team, r);
+      auto all_k = [&](int step) {
+#pragma unroll 1
+        for (int e = 0; e < PER; ++e)
+          widen_k(step, team + 2 * e, e + 1 < PER ? step : step + 1, e + 1 < PER ? team + 2 * e + 2 : team);
+      };
+      if (n_steps > 0) all_k(0);
+      for (int i = 0; i < n_steps; ++i) {
+        if (i + 1 < n_steps) all_k(i + 1);
+#pragma unroll 1
+        for (int e = 0; e < PER; ++e)
+          widen_v(i, team + 2 * e, e + 1 < PER ? i : i + 1, e + 1 < PER ? team + 2 * e + 2 : team);
+      }
     }
     return;
   }
@@ -414,11 +436,10 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     // by constants from the operands' bases.
     const uint32_t q_lo = umma_lo(smem_u32(sQ)), p_lo = umma_lo(smem_u32(sP)), r_lo = umma_lo(smem_u32(ring));
     constexpr uint32_t kS = umma_idesc_f16_f32(M, NKV);
-    const bool lead = lane == 0;
     int slot = 0;
     uint32_t turn = 0;
     auto slot_next = [&]() {
-      if (lead) umma_commit(&b_free[slot]);
+      if (elect_one()) umma_commit(&b_free[slot]);
       if (++slot == NSLOT) slot = 0, turn ^= 1u;
     };
     auto s_step = [&](int i) {
@@ -431,7 +452,7 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
           wait(&b_full[slot], turn);
           tc_fence_after();
           const uint32_t s_lo = r_lo + slot * (C::SLOT >> 4);
-          if (lead) {
+          if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < CW / 16; ++ks) {
               const int kd = c * (CW / 16) + ks;
@@ -442,7 +463,7 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
           slot_next();
         }
       }
-      if (lead) umma_commit(&b_sfull[buf]);
+      if (elect_one()) umma_commit(&b_sfull[buf]);
     };
     // O columns [col, col + N) += P' C over the step's 64 tokens, C rows from descriptor `dims`.
     auto pv = [&](uint32_t col, uint32_t dims, uint32_t idesc, bool keep) {
@@ -460,27 +481,27 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
         wait(&b_full[slot], turn);
         tc_fence_after();
         const uint32_t s_lo = r_lo + slot * (C::SLOT >> 4);
-        if (lead) {
-          if constexpr (C::OR > 0) {
-            if (k == 0) {  // the last chunk: its upper half to S's columns, its lower half to O
-              pv(0, s_lo + (C::OR * 128 >> 4), umma_idesc_f16_f32(M, C::OR), false);
-              umma_commit(&b_tail);
-              pv(C::OCOL + D - CW, s_lo, umma_idesc_f16_f32(M, CW - C::OR), i > 0);
-            } else {
-              pv(C::OCOL + (k - 1) * CW, s_lo, umma_idesc_f16_f32(M, CW), i > 0);
-            }
-          } else {
-            pv(C::OCOL + k * CW, s_lo, umma_idesc_f16_f32(M, CW), i > 0);
+        if (C::OR > 0 && k == NCH - 1) {  // the tail: its first half, and once that has been read its second
+          if (elect_one()) {
+            pv(64 * (i % NS), s_lo, umma_idesc_f16_f32(M, 64), false);
+            umma_commit(&b_tail);
           }
+          wait(&b_tread, i);
+          tc_fence_after();
+          if (elect_one()) {
+            pv(64 * (i % NS), s_lo + (64 * 128 >> 4), umma_idesc_f16_f32(M, 64), false);
+            umma_commit(&b_tail);
+          }
+        } else if (elect_one()) {
+          pv(C::OCOL + k * CW, s_lo, umma_idesc_f16_f32(M, CW), i > 0);
         }
         slot_next();
       }
-      if (lead) umma_commit(&b_pvdone);
+      if (elect_one()) umma_commit(&b_pvdone);
     };
-    if (NS == 2 && n_steps > 0) s_step(0);
+    if (n_steps > 0) s_step(0);
     for (int i = 0; i < n_steps; ++i) {
-      if constexpr (NS == 1) s_step(i);
-      else if (i + 1 < n_steps) s_step(i + 1);
+      if (i + 1 < n_steps) s_step(i + 1);
       pv_step(i);
     }
     __syncwarp();
@@ -491,34 +512,37 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
   regs_inc<C::REG_SOFT>();
   // Softmax state: row tid % 128, columns [32 half, 32 half + 32) of every step.
   float m_used = -INFINITY, l_sum = 0.0f;
-  constexpr int ORH = C::OR / 2;  // tail dims per thread
+  constexpr int ORH = C::OR / 2;  // tail dims per thread: 64 part + 32 half + j at otail[32 part + j]
   float otail[C::OR > 0 ? ORH : 1];
   const int half = warp >> 2, rowi = tid & (M - 1);
   const uint32_t row_tmem = tmem + ((uint32_t)(warp & 3) * 32u << 16);
 
-  {
+  if ((warp & 3) < act) {
     const RowInfo row = sRow[rowi];
 #pragma unroll
     for (int i = 0; i < (C::OR > 0 ? ORH : 1); ++i) otail[i] = 0.0f;
-    auto load_norm = [&](int step) {  // threads 0..63
-      const int64_t pos = (int64_t)(s0 + step) * NKV + tid;
-      return (!ROT && tid < NKV && step < n_steps && pos < seqlen)
+    const int nk = 32 * half + lane;  // the key whose norm this thread fetches for its pair of warps
+    float* const norms = sNorm + (warp & 3) * 2 * NKV;
+    auto load_norm = [&](int step) {
+      const int64_t pos = (int64_t)(s0 + step) * NKV + nk;
+      return (!ROT && step < n_steps && pos < seqlen)
                  ? __half2float(*reinterpret_cast<const __half*>(stream + pos / kTile * C::REC + v_norm_offset(D, B) +
                                                                  2 * (pos % kTile)))
                  : 0.0f;
     };
-    auto add_tail = [&](int step) {  // the last output dims of a step's P' C
+    // The last output dims of a step's P' C: 64 part .. of them, 32 per thread.
+    auto add_tail = [&](int step, int part) {
       if constexpr (C::OR > 0) {
-        wait(&b_tail, step);
+        wait(&b_tail, part);
         tc_fence_after();
         uint32_t tv[32];
-        tmem_ld32(row_tmem + ORH * half, tv);
+        tmem_ld32(row_tmem + 64 * (step % NS) + 32 * half, tv);
         tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b_sfree[0]);
+        if (lane == 0) mbar_arrive(part ? &b_sfree[step % NS] : &b_tread);
 #pragma unroll
-        for (int i = 0; i < ORH; ++i) otail[i] += __uint_as_float(tv[i]);
+        for (int i = 0; i < 32; ++i) otail[32 * part + i] += __uint_as_float(tv[i]);
       }
     };
     constexpr int kFormPlain = 0, kFormCap = 1, kFormAny = 2;
@@ -531,10 +555,10 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     for (int i = 0; i < n_steps; ++i) {
       const int buf = i % NS;
       if constexpr (!ROT) {
-        if (tid < NKV) sNorm[(i & 1) * NKV + tid] = nrm;
+        norms[(i & 1) * NKV + nk] = nrm;
         nrm = load_norm(i + 1);
       }
-      if (i > 0) add_tail(i - 1);
+      if (i > 0) add_tail(i - 1, 0);
       wait(&b_sfull[buf], i / NS);
       tc_fence_after();
       uint32_t sv[32];
@@ -602,10 +626,13 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
       }
       float* const ex = sMax + (i & 1) * 2 * M + rowi;
       ex[half * M] = mx;
-      named_bar(1, C::SOFT);
+      named_bar(1 + (warp & 3), 64);  // the row's two warps
       mx = fmaxf(mx, ex[(1 - half) * M]);
       // P' and (for a rescale) O are free once the step before has been multiplied.
-      if (i > 0) wait(&b_pvdone, i - 1);
+      if (i > 0) {
+        add_tail(i - 1, 1);
+        wait(&b_pvdone, i - 1);
+      }
       tc_fence_after();
       const bool need = mx > m_used + 2.0f;  // also when m_used is -inf and a key is seen
       if (__any_sync(0xffffffffu, need)) {
@@ -630,7 +657,7 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
       const float mref = (m_used == -INFINITY) ? 0.0f : m_used;  // nothing seen yet: every x is -inf
       uint64_t ps = f32x2(0.0f, 0.0f);
       const uint64_t zA2 = f32x2(zA, zA), zC2 = f32x2(zC - mref, zC - mref);
-      const float4* n4 = reinterpret_cast<const float4*>(sNorm + (i & 1) * NKV + 32 * half);
+      const float4* n4 = reinterpret_cast<const float4*>(norms + (i & 1) * NKV + 32 * half);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t hi[4], lo[4];
@@ -675,14 +702,15 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
       if (lane == 0) mbar_arrive(&b_pfull);
     }
     if (n_steps > 0) {
-      add_tail(n_steps - 1);
+      add_tail(n_steps - 1, 0);
+      add_tail(n_steps - 1, 1);
       wait(&b_pvdone, n_steps - 1);
       tc_fence_after();
     }
     // The row's sum: both halves'.
     float* const ex = sMax + (n_steps & 1) * 2 * M + rowi;
     ex[half * M] = l_sum;
-    named_bar(1, C::SOFT);
+    named_bar(1 + (warp & 3), 64);  // the row's two warps
     l_sum += ex[(1 - half) * M];
   }
 
@@ -700,10 +728,10 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     else slot[(int64_t)M * D + tid] = lse;
   }
   tc_fence_before();
-  named_bar(1, C::SOFT);
+  named_bar(5, C::SOFT);
   tc_fence_after();
   for (int r0 = 0; r0 < rows; r0 += C::RP) {
-    if ((warp & 3) * 32 >= r0 && (warp & 3) * 32 < r0 + C::RP) {
+    if ((warp & 3) < act && (warp & 3) * 32 >= r0 && (warp & 3) * 32 < r0 + C::RP) {
       float* const dst = stage + (rowi - r0) * C::STRIDE;
 #pragma unroll 1
       for (int c = half * (C::OT / 2); c < (half + 1) * (C::OT / 2); c += 32) {
@@ -722,12 +750,12 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
       if constexpr (C::OR > 0) {
 #pragma unroll
         for (int k = 0; k < ORH; k += 4)
-          *reinterpret_cast<float4*>(dst + C::OT + ORH * half + k) =
+          *reinterpret_cast<float4*>(dst + C::OT + 64 * (k / 32) + 32 * half + k % 32) =
               inv > 0.0f ? make_float4(otail[k] * inv, otail[k + 1] * inv, otail[k + 2] * inv, otail[k + 3] * inv)
                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
     }
-    named_bar(1, C::SOFT);
+    named_bar(5, C::SOFT);
     for (int r = r0 + warp; r < min(rows, r0 + C::RP); r += C::SOFT / 32) {
       float2 v[D / 64];
 #pragma unroll
@@ -742,7 +770,7 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
         derotate_store_row<D>(v, lane, nullptr, slot + (int64_t)r * D);
       }
     }
-    named_bar(1, C::SOFT);
+    named_bar(5, C::SOFT);
   }
   if (warp == 0) tmem_dealloc(tmem, 512);
 }

@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 
 #include "../../include/ckv.h"
@@ -80,14 +81,15 @@ ckv_status check_cache(const ckv_cache* c) {
 
 // Split count: one CTA per SM in a single wave (measured best: a CTA streams
 // its splits' tiles through the whole kernel); no more splits than tiles.
-int auto_split(int64_t units, int64_t max_seq_len, int tiles_per_cta_iter) {
+// ctas_per_sm: CTAs of the kernel that share an SM.
+int auto_split(int64_t units, int64_t max_seq_len, int tiles_per_cta_iter, int ctas_per_sm = 1) {
   const int64_t tiles = (max_seq_len + 15) / 16;
   if (tiles == 0) return 1;
   // A sequence that one CTA covers in two iterations runs as one split: its
   // rows then go straight to the output, with no merge (a 256-token decode at
   // head dim 128: 6.96 us in one split against 8.74 in two).
   if (tiles <= 2 * tiles_per_cta_iter) return 1;
-  const int sms = num_sms();
+  const int64_t sms = static_cast<int64_t>(num_sms()) * ctas_per_sm;
   int64_t s = sms / units;
   const int64_t by_tiles = (tiles + tiles_per_cta_iter - 1) / tiles_per_cta_iter;
   if (s > by_tiles) s = by_tiles;
@@ -932,7 +934,8 @@ static ckv_status plan_scored(const ckv_cache* cache, int64_t max_seq_len, int n
   if (bh > 65535) return fail(CKV_ERR_UNSUPPORTED, "batch * n_kv_heads above 65535");
   const int G = n_q_heads / cache->n_kv_heads;
   const size_t row = sizeof(float);
-  sp->tiles = static_cast<int64_t>(G) * n_q > kTileRows && G <= 128;
+  static const int dbg = getenv("CKV_TR") ? atoi(getenv("CKV_TR")) : kTileRows;
+  sp->tiles = static_cast<int64_t>(G) * n_q > dbg && G <= 128;
   sp->n_row_groups = p.n_row_groups;
   sp->groups = p.groups;
   if (sp->tiles) {
@@ -950,7 +953,7 @@ static ckv_status plan_scored(const ckv_cache* cache, int64_t max_seq_len, int n
     sp->ws = 256 + (ns == 1 ? 0 : static_cast<size_t>(units) * ns * 128 * (cache->head_dim + 1) * row);
     return CKV_OK;
   }
-  sp->n_split = n_split ? n_split : auto_split(p.groups, keys, cache->head_dim == 512 ? 4 : 8);
+  sp->n_split = n_split ? n_split : auto_split(p.groups, keys, cache->head_dim == 512 ? 4 : 8, cache->head_dim <= 128 ? 2 : 1);
   sp->part = ws_header_bytes(p.groups, sp->n_split);
   sp->ws = sp->n_split == 1 ? sp->part : decode_ws_bytes(cache->head_dim, p.groups, sp->n_split);
   return CKV_OK;
