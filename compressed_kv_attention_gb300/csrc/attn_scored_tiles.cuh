@@ -243,44 +243,57 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     auto slot_done = [&](int g) {
       if (lane == 0) mbar_arrive(&b_full[g % NSLOT]);
     };
+    auto step_base = [&](int step) { return stream + (int64_t)(s0 + step) * (4 * C::REC); };
+    // Records of a step that lie inside the cache (4 but for its end).
+    auto step_recs = [&](int step) {
+      return step < n_steps ? static_cast<int>(min((int64_t)4, n_rec - (int64_t)(s0 + step) * 4)) : 0;
+    };
     // K chunk c of a step: 4 records x CW / 32 blocks x 32 lanes of 16 bytes,
-    // each 8 dims of tokens kpp and kpp + 8 of a record.
-    constexpr int PIECES = 4 * (CW / 32) * 32, KR = PIECES / C::TEAM;
-    static_assert(KR >= 1 && PIECES % C::TEAM == 0, "K pieces per thread");
+    // each 8 dims of tokens kpp and kpp + 8 of a record. A warp has one block
+    // and the records k_rec + r KS, r < KR.
+    constexpr int NBLK = CW / 32, KS = 4 / NBLK, KR = 4 / KS;
     const int kq = lane >> 3, kpp = lane & 7;
+    const int k_blk = (tw >> 5) % NBLK, k_rec = (tw >> 5) / NBLK;
+    const int k_src = k_rec * C::REC + (k_blk * 32 + 4 * kpp + kq) * 16;
+    const int k_sc = k_rec * C::REC + k_scale_offset(D) + 2 * (kpp * C::NB + k_blk);
+    const uint32_t k_dst = sw128_offset(k_rec * kTile + kpp, k_blk * 32 + 8 * kq, NKV);  // + 128 per row
     uint4 kw[KR];
     uint32_t ks[KR];  // the two tokens' scales
-    auto fetch_k = [&](int step, int c, int r) {
-      const int u = r * (C::TEAM / 32) + (tw >> 5);  // (record, block) of this warp
-      const int64_t rec = (int64_t)(s0 + step) * 4 + u / (CW / 32);
-      const int blk = c * (CW / 32) + u % (CW / 32);
-      if (step < n_steps && rec < n_rec) {
-        const uint8_t* p = stream + rec * C::REC;
-        kw[r] = *reinterpret_cast<const uint4*>(p + (blk * 32 + 4 * kpp + kq) * 16);
-        const uint16_t* sc = reinterpret_cast<const uint16_t*>(p + k_scale_offset(D)) + blk;
-        ks[r] = sc[kpp * C::NB] | (uint32_t)sc[(kpp + 8) * C::NB] << 16;
-      } else {
-        kw[r] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-        ks[r] = 0u;
+    auto fetch_k = [&](int step, int c) {
+      const uint8_t* p = step_base(step);
+      const int recs = step_recs(step);
+#pragma unroll
+      for (int r = 0; r < KR; ++r) {
+        if (k_rec + r * KS < recs) {
+          const int at = r * KS * C::REC;
+          kw[r] = *reinterpret_cast<const uint4*>(p + k_src + at + c * (NBLK * 512));
+          const uint8_t* sc = p + k_sc + at + c * (NBLK * 2);
+          ks[r] = *reinterpret_cast<const uint16_t*>(sc) |
+                  (uint32_t)*reinterpret_cast<const uint16_t*>(sc + 16 * C::NB) << 16;
+        } else {
+          kw[r] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
+          ks[r] = 0u;
+        }
       }
     };
     // Widens the fetched chunk c of `step` and fetches (step_n, c_n).
     auto widen_k = [&](int step, int c, int step_n, int c_n) {
       const int g = k_index(step, c);
+      uint4 w4[KR];
+      uint32_t sc[KR];
+#pragma unroll
+      for (int r = 0; r < KR; ++r) w4[r] = kw[r], sc[r] = ks[r];
+      fetch_k(step_n, c_n);
       slot_wait(g);
       slot_wait(g + 1);
-      uint8_t* const s_hi = ring + g % NSLOT * C::SLOT;
-      uint8_t* const s_lo = ring + (g + 1) % NSLOT * C::SLOT;
+      uint8_t* const s_hi = ring + g % NSLOT * C::SLOT + k_dst;
+      uint8_t* const s_lo = ring + (g + 1) % NSLOT * C::SLOT + k_dst;
 #pragma unroll
       for (int r = 0; r < KR; ++r) {
-        const int u = r * (C::TEAM / 32) + (tw >> 5);
-        const int row0 = u / (CW / 32) * kTile + kpp, k0 = (u % (CW / 32)) * 32 + 8 * kq;
-        const uint32_t w[4] = {kw[r].x, kw[r].y, kw[r].z, kw[r].w};
-        const uint32_t sc = ks[r];
-        fetch_k(step_n, c_n, r);
+        const uint32_t w[4] = {w4[r].x, w4[r].y, w4[r].z, w4[r].w};
 #pragma unroll
         for (int hs = 0; hs < 2; ++hs) {
-          const uint32_t dd = __byte_perm(sc, 0u, hs ? 0x3232 : 0x1010);
+          const uint32_t dd = __byte_perm(sc[r], 0u, hs ? 0x3232 : 0x1010);
           const __half2 d2 = *reinterpret_cast<const __half2*>(&dd);
           uint32_t qh[4], hi[4], lo[4];
           i8x4_to_half2x2(w[2 * hs], qh[0], qh[1]);
@@ -293,9 +306,9 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
             hi[e] = *reinterpret_cast<const uint32_t*>(&h);
             lo[e] = *reinterpret_cast<const uint32_t*>(&l);
           }
-          const uint32_t off = sw128_offset(row0 + 8 * hs, k0, NKV);
-          *reinterpret_cast<uint4*>(s_hi + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(s_lo + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          const int row = (r * KS * kTile + 8 * hs) * 128;
+          *reinterpret_cast<uint4*>(s_hi + row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(s_lo + row) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
       fence_proxy_async();
@@ -304,34 +317,43 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
       slot_done(g + 1);
     };
     // V chunk c of a step: units of (lane stream, 8 dims), 16 fields of 2B
-    // bits in B words of the stream. Unit v = 16 part + 4 record + (stream % 4).
-    constexpr int GDIM = D / 8;                             // dims per lane stream
-    constexpr int SUB = GDIM / 8;                           // 8-dim parts of a stream
+    // bits in B words of the stream. Unit v = 16 part + 4 record + (stream % 4),
+    // part = v_part + 8 r of the chunk.
+    constexpr int SUB = D / 64;                             // 8-dim parts of a lane stream
     constexpr int VR = 16 * (CW / 8) / C::TEAM;             // units per thread and chunk
     static_assert(VR >= 1, "V units per thread");
-    const int v_rec = (tw >> 2) & 3, v_t = tw & 3;
+    const int v_rec = (tw >> 2) & 3, v_t = tw & 3, v_part = tw >> 4;
     constexpr int GR = v_granule(D, B);
     uint32_t vw[VR][B], vn[VR][2];
-    auto fetch_v = [&](int step, int c, int r) {
-      const int part = c * (CW / 8) + (tw >> 4) + r * (C::TEAM / 16);  // dims 8 part .. 8 part + 7
-      const int L = 4 * (part / SUB) + v_t, w0 = (part % SUB) * B;
-      const int64_t rec = (int64_t)(s0 + step) * 4 + v_rec;
-      const bool in = step < n_steps && rec < n_rec;
-      const uint8_t* p = stream + rec * C::REC;
+    auto fetch_v = [&](int step, int c) {
+      const uint8_t* p = step_base(step) + v_rec * C::REC;
+      const bool in = v_rec < step_recs(step);
 #pragma unroll
-      for (int w = 0; w < B; ++w) {
-        const int sb = 4 * (w0 + w);
-        vw[r][w] = in ? *reinterpret_cast<const uint32_t*>(p + v_code_offset(D) + ((sb / GR) * 32 + L) * GR + sb % GR) : 0u;
-      }
-      if constexpr (ROT) {  // the norms of positions 2t, 2t + 1 and 2t + 8, 2t + 9
-        const uint8_t* nb = p + v_norm_offset(D, B) + 2 * (kTile * (8 * part / kRotGroup) + 2 * v_t);
-        vn[r][0] = in ? *reinterpret_cast<const uint32_t*>(nb) : 0u;
-        vn[r][1] = in ? *reinterpret_cast<const uint32_t*>(nb + 16) : 0u;
+      for (int r = 0; r < VR; ++r) {
+        const int part = c * (CW / 8) + v_part + 8 * r;  // dims 8 part .. 8 part + 7
+        const int L = 4 * (part / SUB) + v_t, w0 = (part % SUB) * B;
+#pragma unroll
+        for (int w = 0; w < B; ++w) {
+          const int sb = 4 * (w0 + w);
+          vw[r][w] = in ? *reinterpret_cast<const uint32_t*>(p + v_code_offset(D) + (sb / GR * 32 + L) * GR + sb % GR) : 0u;
+        }
+        if constexpr (ROT) {  // the norms of positions 2t, 2t + 1 and 2t + 8, 2t + 9
+          const uint8_t* nb = p + v_norm_offset(D, B) + 2 * (kTile * (8 * part / kRotGroup) + 2 * v_t);
+          vn[r][0] = in ? *reinterpret_cast<const uint32_t*>(nb) : 0u;
+          vn[r][1] = in ? *reinterpret_cast<const uint32_t*>(nb + 16) : 0u;
+        }
       }
     };
     auto widen_v = [&](int step, int c, int step_n, int c_n) {
-      uint32_t keep[2] = {~0u, ~0u};  // norms of positions that no row sees may hold any bytes
-      if constexpr (ROT) {
+      uint32_t wv[VR][B], nv[VR][2];
+#pragma unroll
+      for (int r = 0; r < VR; ++r) {
+#pragma unroll
+        for (int e = 0; e < B; ++e) wv[r][e] = vw[r][e];
+        if constexpr (ROT) nv[r][0] = vn[r][0], nv[r][1] = vn[r][1];
+      }
+      fetch_v(step_n, c_n);
+      if constexpr (ROT) {  // norms of positions that no row sees may hold any bytes
         const int pos0 = (s0 + step) * NKV;
         if (pos0 < flo || pos0 + NKV > fhi) {
           uint32_t any = 0u;
@@ -342,41 +364,39 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
             if (rec == v_rec) any = m;
           }
           const uint32_t ma = any >> (2 * v_t), mb = any >> (2 * v_t + 8);
-          keep[0] = (ma & 1u ? 0xffffu : 0u) | (ma & 2u ? 0xffff0000u : 0u);
-          keep[1] = (mb & 1u ? 0xffffu : 0u) | (mb & 2u ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int r = 0; r < VR; ++r) {
+            nv[r][0] &= (ma & 1u ? 0xffffu : 0u) | (ma & 2u ? 0xffff0000u : 0u);
+            nv[r][1] &= (mb & 1u ? 0xffffu : 0u) | (mb & 2u ? 0xffff0000u : 0u);
+          }
         }
       }
       const int g = v_index(step, c);
       slot_wait(g);
-      uint8_t* const dst = ring + g % NSLOT * C::SLOT;
       const uint32_t lut = smem_u32(sLut) + (uint32_t)(lane << 2);
-      const int tok = v_rec * kTile + 2 * v_t;
+      // Row 8 part + d of the slot, position 16 v_rec + 2 v_t + 8 h: 16-byte
+      // unit 2 v_rec + h, swizzled by the row. A warp holds two parts, whose rows
+      // share their banks: one stores h while the other stores 1 - h.
+      const uint32_t flip = v_part & 1;
+      const uint32_t dst = smem_u32(ring + g % NSLOT * C::SLOT) + v_part * 1024 + ((2 * v_rec + flip) << 4) + 4 * v_t;
 #pragma unroll
       for (int r = 0; r < VR; ++r) {
-        const int v_part = (tw >> 4) + r * (C::TEAM / 16);  // 8-dim part of the chunk
-        uint32_t w[B], nn[2] = {ROT ? vn[r][0] & keep[0] : 0u, ROT ? vn[r][1] & keep[1] : 0u};
-#pragma unroll
-        for (int e = 0; e < B; ++e) w[e] = vw[r][e];
-        fetch_v(step_n, c_n, r);
         auto field = [&](int f) {  // dim 2 (f / 4) + (f & 1), positions + 8 (f >> 1 & 1)
           uint32_t val;
           if constexpr (B == 3) {
             const int bit = 6 * f, wi = bit >> 5, sh = bit & 31;
-            uint32_t y = w[wi] >> sh;
-            if (sh > 26 && wi + 1 < B) y |= w[wi + 1 < B ? wi + 1 : wi] << (32 - sh);
+            uint32_t y = wv[r][wi] >> sh;
+            if (sh > 26 && wi + 1 < B) y |= wv[r][wi + 1 < B ? wi + 1 : wi] << (32 - sh);
             val = lds32(lut + ((y & 63u) << 7));
           } else if constexpr (B == 2) {
-            val = lds32(lut + (((w[f >> 3] >> (4 * (f & 7))) & 15u) << 7));
+            val = lds32(lut + (((wv[r][f >> 3] >> (4 * (f & 7))) & 15u) << 7));
           } else {
-            const uint32_t y = (w[f >> 2] >> (8 * (f & 3))) & 255u;
+            const uint32_t y = (wv[r][f >> 2] >> (8 * (f & 3))) & 255u;
             val = __byte_perm(lds32(lut + ((y & 15u) << 7)), lds32(lut + ((y >> 4) << 7)), 0x7610);
           }
-          if constexpr (ROT) val = hmul2_u32(val, nn[f >> 1 & 1]);
+          if constexpr (ROT) val = hmul2_u32(val, nv[r][f >> 1 & 1]);
           return val;
         };
-        // A warp holds two parts, whose rows share their banks: one writes the
-        // upper eight positions of a record while the other writes the lower.
-        const bool flip = v_part & 1;
         // Eight lookups in flight, then their stores.
 #pragma unroll
         for (int f0 = 0; f0 < 16; f0 += 8) {
@@ -385,9 +405,10 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
           for (int f = 0; f < 8; ++f) val[f] = field(f0 + f);
 #pragma unroll
           for (int f = 0; f < 8; ++f) {
-            const int dim = v_part * 8 + 2 * ((f0 + f) >> 2) + (f & 1), h = f >> 1 & 1;
-            *reinterpret_cast<uint32_t*>(dst + sw128_offset(dim, tok + 8 * (flip ? 1 - h : h), CW)) =
-                flip ? val[f ^ 2] : val[f];
+            const int d = 2 * ((f0 + f) >> 2) + (f & 1), h = f >> 1 & 1;
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"((dst ^ (uint32_t)((d ^ h) << 4)) + 128 * d + 8192 * r),
+                         "r"(flip ? val[f ^ 2] : val[f])
+                         : "memory");
           }
         }
       }
@@ -397,20 +418,16 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     };
     if constexpr (NCH == 1) {
       if (team == 0) {
-#pragma unroll
-        for (int r = 0; r < KR; ++r) fetch_k(0, 0, r);
+        fetch_k(0, 0);
         for (int i = 0; i < n_steps; ++i) widen_k(i, 0, i + 1, 0);
       } else {
-#pragma unroll
-        for (int r = 0; r < VR; ++r) fetch_v(0, 0, r);
+        fetch_v(0, 0);
         for (int i = 0; i < n_steps; ++i) widen_v(i, 0, i + 1, 0);
       }
     } else {
       constexpr int PER = NCH / 2;  // chunks of a step per team: team, team + 2, ...
-#pragma unroll
-      for (int r = 0; r < KR; ++r) fetch_k(0, team, r);
-#pragma unroll
-      for (int r = 0; r < VR; ++r) fetch_v(0, team, r);
+      fetch_k(0, team);
+      fetch_v(0, team);
       auto all_k = [&](int step) {
 #pragma unroll 1
         for (int e = 0; e < PER; ++e)
@@ -558,7 +575,10 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
         norms[(i & 1) * NKV + nk] = nrm;
         nrm = load_norm(i + 1);
       }
-      if (i > 0) add_tail(i - 1, 0);
+      if (i > 0) {  // at once: S of the next step waits for these columns
+        add_tail(i - 1, 0);
+        add_tail(i - 1, 1);
+      }
       wait(&b_sfull[buf], i / NS);
       tc_fence_after();
       uint32_t sv[32];
@@ -629,10 +649,7 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
       named_bar(1 + (warp & 3), 64);  // the row's two warps
       mx = fmaxf(mx, ex[(1 - half) * M]);
       // P' and (for a rescale) O are free once the step before has been multiplied.
-      if (i > 0) {
-        add_tail(i - 1, 1);
-        wait(&b_pvdone, i - 1);
-      }
+      if (i > 0) wait(&b_pvdone, i - 1);
       tc_fence_after();
       const bool need = mx > m_used + 2.0f;  // also when m_used is -inf and a key is seen
       if (__any_sync(0xffffffffu, need)) {
