@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     }
   }
   griddep_wait();
+  griddep_launch_dependents();  // the merge waits for this grid's end before it reads
 
   // ---- rows, their common span [glo, ghi), and the part [flo, fhi) that every row sees ----
   int seqlen, n;
@@ -178,23 +179,32 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     if (lane == 0) s_red[warp][0] = lo0, s_red[warp][1] = hi1, s_red[warp][2] = lo1, s_red[warp][3] = hi0;
   }
   // ---- Q to shared memory: fp16 (bf16 is converted, exact within fp16's range) ----
-  for (int piece = tid; piece < M * (D / 8); piece += C::THREADS) {
-    const int r = piece / (D / 8), k0 = (piece % (D / 8)) * 8;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (r < rows) {
-      const int64_t qrow = ((int64_t)b * a.n_q + q0 + r / G) * a.n_q_heads + kvh * G + r % G;
-      v = __ldg(reinterpret_cast<const uint4*>(a.q + qrow * D + k0));
-      if (a.q_bf16) {
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  // Four loads in flight per thread (the rows' latency is the start of the CTA).
+  for (int p0 = tid; p0 < M * (D / 8); p0 += 4 * C::THREADS) {
+    uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
-          w[i] = pack_half2(__low2float(x), __high2float(x));
-        }
-        v = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i) {
+      const int piece = p0 + i * C::THREADS, r = piece / (D / 8), k0 = (piece % (D / 8)) * 8;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int64_t qrow = ((int64_t)b * a.n_q + q0 + r / G) * a.n_q_heads + kvh * G + r % G;
+        v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + qrow * D + k0));
       }
     }
-    *reinterpret_cast<uint4*>(sQ + sw128_offset(r, k0, M)) = v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int piece = p0 + i * C::THREADS, r = piece / (D / 8), k0 = (piece % (D / 8)) * 8;
+      if (a.q_bf16) {
+        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
+          w[e] = pack_half2(__low2float(x), __high2float(x));
+        }
+        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (r < M) *reinterpret_cast<uint4*>(sQ + sw128_offset(r, k0, M)) = v[i];
+    }
   }
   // P' of the row groups without a real row stays zero.
   for (int e = act * 32 * 8 + tid; e < M * 8; e += C::THREADS) {
@@ -793,14 +803,17 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
 }
 
 // The n_split partials of every output row, merged exactly (log-sum-exp), and
-// the inverse transform: one CTA of 128 threads per row, the row's slots read
-// 16 bytes per thread with several in flight.
+// the inverse transform: one CTA per row. The partials sit in L2: every thread
+// takes one 16-byte unit of the row over a strided subset of the slots with all
+// its loads (up to 20) in flight before the weights are known, so that the
+// merge costs about one round trip.
+constexpr int kScoredMergeThreads = 512;
 template <int D, int B, int ROT>
-__global__ void __launch_bounds__(128) scored_merge_rows_kernel(ScoredArgs a) {
-  constexpr int M = 128, UNITS = D / 4, SG = 128 / UNITS > 0 ? 128 / UNITS : 1, PER = 8;
+__global__ void __launch_bounds__(kScoredMergeThreads) scored_merge_rows_kernel(ScoredArgs a) {
+  constexpr int M = 128, NT = kScoredMergeThreads, UNITS = D / 4, SG = NT / UNITS, PER = 20;
   constexpr int64_t SLOT = M * (int64_t)(D + 1);
   __shared__ float s_w[kMaxSplits];
-  __shared__ float s_red[4];
+  __shared__ float s_red[NT / 32];
   __shared__ __align__(16) float4 s_acc[SG][UNITS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_wait();
@@ -810,10 +823,20 @@ __global__ void __launch_bounds__(128) scored_merge_rows_kernel(ScoredArgs a) {
   const int64_t bq = r / a.n_q_heads;
   const int qi = static_cast<int>(bq % a.n_q), b = static_cast<int>(bq / a.n_q);
   const int64_t tile = ((int64_t)b * a.n_kv_heads + h / G) * n_qt + (n_qt - 1 - qi / QT);
-  const int rin = (qi % QT) * G + h % G;
-  const float* const base = a.part + tile * a.n_split * SLOT;
+  const int rin = (qi % QT) * G + h % G, n_split = a.n_split;
+  const float* const base = a.part + tile * n_split * SLOT;
+  const int u = tid % UNITS, g = tid / UNITS;
+  float4 x[PER];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int s = s0 + g + j * SG;
+      if (s < n_split) x[j] = __ldcg(reinterpret_cast<const float4*>(base + s * SLOT + (int64_t)rin * D) + u);
+    }
+  };
+  load(0);
   float m = -INFINITY;
-  for (int s = tid; s < a.n_split; s += 128) {
+  for (int s = tid; s < n_split; s += NT) {
     const float l = __ldcg(base + s * SLOT + (int64_t)M * D + rin);
     s_w[s] = l;
     m = fmaxf(m, l);
@@ -822,47 +845,100 @@ __global__ void __launch_bounds__(128) scored_merge_rows_kernel(ScoredArgs a) {
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) s_red[warp] = m;
   __syncthreads();
-  m = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-  float total = 0.0f;
-  for (int s = 0; s < a.n_split; ++s) total += (s_w[s] == -INFINITY) ? 0.0f : exp2f((s_w[s] - m) * 1.4426950408889634f);
-  const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-  const int u = tid % UNITS, g = tid / UNITS;
+  m = s_red[0];
+#pragma unroll
+  for (int w = 1; w < NT / 32; ++w) m = fmaxf(m, s_red[w]);
+  for (int s = tid; s < n_split; s += NT) s_w[s] = (s_w[s] == -INFINITY) ? 0.0f : exp2f((s_w[s] - m) * 1.4426950408889634f);
+  __syncthreads();
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (g < SG) {
-    for (int s0 = g; s0 < a.n_split; s0 += SG * PER) {
-      float4 x[PER];
+  for (int s0 = 0; s0 < n_split; s0 += PER * SG) {
+    if (s0 > 0) load(s0);
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const int s = s0 + j * SG;
-        if (s < a.n_split) x[j] = __ldcg(reinterpret_cast<const float4*>(base + s * SLOT + (int64_t)rin * D) + u);
-      }
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const int s = s0 + j * SG;
-        if (s < a.n_split) {
-          const float w = (s_w[s] == -INFINITY) ? 0.0f : exp2f((s_w[s] - m) * 1.4426950408889634f) * inv;
-          acc.x = fmaf(w, x[j].x, acc.x);
-          acc.y = fmaf(w, x[j].y, acc.y);
-          acc.z = fmaf(w, x[j].z, acc.z);
-          acc.w = fmaf(w, x[j].w, acc.w);
-        }
+    for (int j = 0; j < PER; ++j) {
+      const int s = s0 + g + j * SG;
+      if (s < n_split) {
+        const float w = s_w[s];
+        acc.x = fmaf(w, x[j].x, acc.x);
+        acc.y = fmaf(w, x[j].y, acc.y);
+        acc.z = fmaf(w, x[j].z, acc.z);
+        acc.w = fmaf(w, x[j].w, acc.w);
       }
     }
-    s_acc[g][u] = acc;
   }
+  s_acc[g][u] = acc;
   __syncthreads();
   if (warp) return;
+  float total = 0.0f;
+  for (int s = lane; s < n_split; s += 32) total += s_w[s];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const float inv = total > 0.0f ? 1.0f / total : 0.0f;
   const float* flat = reinterpret_cast<const float*>(s_acc);
   float2 v[D / 64];
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) {
-    v[e] = make_float2(0.0f, 0.0f);
+    float2 y = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < SG; ++k) {
-      const float2 y = *reinterpret_cast<const float2*>(flat + k * D + 64 * e + 2 * lane);
-      v[e].x += y.x;
-      v[e].y += y.y;
+      const float2 z = *reinterpret_cast<const float2*>(flat + k * D + 64 * e + 2 * lane);
+      y.x += z.x;
+      y.y += z.y;
     }
+    v[e] = make_float2(y.x * inv, y.y * inv);
+  }
+  float* const o = a.out_type == kOutF32 ? a.out + r * D
+                                         : reinterpret_cast<float*>(reinterpret_cast<uint16_t*>(a.out) + r * D);
+  derotate_store_row<D, ROT, true>(v, lane, a.signs, o, centroid_scale(B), a.signs2, a.out_type);
+  if (lane == 0) a.lse[r] = total > 0.0f ? m + logf(total) : -INFINITY;
+}
+
+// The same for few splits (at most 32), where rows are many: one warp per row.
+template <int D, int B, int ROT>
+__global__ void __launch_bounds__(256) scored_merge_few_kernel(ScoredArgs a) {
+  constexpr int M = 128, PER = 4;
+  constexpr int64_t SLOT = M * (int64_t)(D + 1);
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  griddep_wait();
+  if (r >= (int64_t)a.batch * a.n_q * a.n_q_heads) return;
+  const int G = a.n_q_heads / a.n_kv_heads, QT = M / G, n_qt = (a.n_q + QT - 1) / QT;
+  const int h = static_cast<int>(r % a.n_q_heads);
+  const int64_t bq = r / a.n_q_heads;
+  const int qi = static_cast<int>(bq % a.n_q), b = static_cast<int>(bq / a.n_q);
+  const int64_t tile = ((int64_t)b * a.n_kv_heads + h / G) * n_qt + (n_qt - 1 - qi / QT);
+  const int rin = (qi % QT) * G + h % G;
+  const float* const base = a.part + tile * a.n_split * SLOT;
+  const float l = lane < a.n_split ? __ldcg(base + lane * SLOT + (int64_t)M * D + rin) : -INFINITY;
+  float m = l;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float w = (l == -INFINITY) ? 0.0f : exp2f((l - m) * 1.4426950408889634f);
+  float total = w;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+  float2 v[D / 64];
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) v[e] = make_float2(0.0f, 0.0f);
+  for (int s0 = 0; s0 < a.n_split; s0 += PER) {
+    float2 x[PER][D / 64];
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (s0 + j < a.n_split) {
+        const float2* src = reinterpret_cast<const float2*>(base + (s0 + j) * SLOT + (int64_t)rin * D) + lane;
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) x[j][e] = __ldcg(src + 32 * e);
+      }
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+      if (s0 + j < a.n_split) {
+        const float ws = __shfl_sync(0xffffffffu, w, s0 + j) * inv;
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) {
+          v[e].x = fmaf(ws, x[j][e].x, v[e].x);
+          v[e].y = fmaf(ws, x[j][e].y, v[e].y);
+        }
+      }
   }
   float* const o = a.out_type == kOutF32 ? a.out + r * D
                                          : reinterpret_cast<float*>(reinterpret_cast<uint16_t*>(a.out) + r * D);
@@ -895,9 +971,15 @@ static cudaError_t launch_scored_tiles_d(const ScoredArgs& a, cudaStream_t strea
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, attn_scored_tiles_kernel<D, B, ROT>, a);
   if (e != cudaSuccess || a.n_split == 1) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>((int64_t)a.batch * a.n_q * a.n_q_heads));
-  cfg.blockDim = dim3(128);
+  const int64_t out_rows = (int64_t)a.batch * a.n_q * a.n_q_heads;
   cfg.dynamicSmemBytes = 0;
+  if (a.n_split <= 32) {
+    cfg.gridDim = dim3(static_cast<unsigned>((out_rows + 7) / 8));
+    cfg.blockDim = dim3(256);
+    return cudaLaunchKernelEx(&cfg, scored_merge_few_kernel<D, B, ROT>, a);
+  }
+  cfg.gridDim = dim3(static_cast<unsigned>(out_rows));
+  cfg.blockDim = dim3(kScoredMergeThreads);
   return cudaLaunchKernelEx(&cfg, scored_merge_rows_kernel<D, B, ROT>, a);
 }
 
