@@ -94,11 +94,6 @@ __global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, CScored<D, B, ROT
   griddep_wait();
   griddep_launch_dependents();
 
-  int seqlen, n;
-  scored_lengths(a, b, threadIdx.x == 0, seqlen, n);
-  const int base = seqlen - n;
-  if (threadIdx.x < 8) s_row[threadIdx.x] = scored_row(a, b, kvh, rg * 8 + threadIdx.x, seqlen, n);
-  if (warp >= 2 && warp < 4) scored_depths(a, b, n, threadIdx.x - 64, s_depth);
   uint32_t qf[C::NB_W][4];
   {
     const int rr = rg * 8 + (lane >> 2);
@@ -108,6 +103,13 @@ __global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, CScored<D, B, ROT
     load_q_frags<C::NB_W>(qf, a.q + ((int64_t)(b * a.n_q + qi) * a.n_q_heads + h) * D, ok, wh * C::NB_W, lane & 3);
     if (a.q_bf16) convert_q_frags<C::NB_W>(qf);
   }
+  RowLoads in{0.0f, 0, 0, 0ull};
+  if (threadIdx.x < 8) in = scored_row_loads(a, b, kvh, rg * 8 + threadIdx.x);
+  int seqlen, n;
+  scored_lengths(a, b, threadIdx.x == 0, seqlen, n);
+  const int base = seqlen - n;
+  if (threadIdx.x < 8) s_row[threadIdx.x] = scored_row(a, b, rg * 8 + threadIdx.x, in, seqlen, n);
+  if (warp >= 2 && warp < 4) scored_depths(a, b, n, threadIdx.x - 64, s_depth);
   __syncthreads();
 
   // The CTA's keys: the union [glo, ghi) of its rows' intervals, cut into

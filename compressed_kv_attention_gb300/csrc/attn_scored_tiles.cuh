@@ -77,8 +77,8 @@ struct CTiles {
   static_assert(2 * REG_SOFT + 2 * REG_WIDEN + REG_MMA <= 5 * 96, "the roles share the launch's registers");
   // Output staging of the epilogue: RP rows at a time, padded by 16 bytes.
   static constexpr int STRIDE = D + 4;
-  static constexpr int RP = 64 * STRIDE * 4 <= LUT_OFF ? 64 : 32;
-  static_assert(RP * STRIDE * 4 <= LUT_OFF, "staging fits the operands' memory");
+  static constexpr int RP = 131 * STRIDE * 4 <= LUT_OFF ? 128 : 64 + 3 <= LUT_OFF / (STRIDE * 4) ? 64 : 32;
+  static_assert((RP + 3) * STRIDE * 4 <= LUT_OFF, "staging (and the last rows' neighbours) inside the operands' memory");
 };
 
 }  // namespace
@@ -149,27 +149,20 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     s_abort = 0;
     fence_barrier_init();
   }
-  {
-    constexpr float inv = 1.0f / centroid_scale(B);
-    for (int e = tid; e < C::LUT * 32; e += C::THREADS) {
-      const int f = e >> 5;
-      const int klo = (B == 4) ? f : (f & ((1 << B) - 1));
-      const int khi = (B == 4) ? f : (f >> B);
-      sLut[e] = pack_half2(tbq_centroid<B>(klo) * inv, tbq_centroid<B>(khi) * inv);
-    }
-  }
   griddep_wait();
   griddep_launch_dependents();  // the merge waits for this grid's end before it reads
 
   // ---- rows, their common span [glo, ghi), and the part [flo, fhi) that every row sees ----
+  // Warps 0-3 form the rows while the others load Q and fill the value table.
+  RowLoads in{0.0f, 0, 0, 0ull};
+  if (tid < rows) in = scored_row_loads(a, b, kvh, q0 * G + tid);
   int seqlen, n;
   scored_lengths(a, b, tid == 0, seqlen, n);
   const int base = seqlen - n;
   const bool tree = a.tree != nullptr;
-  if (tid >= 128 && tid < 192) scored_depths(a, b, n, tid - 128, s_depth);
   if (tid < M) {
     RowInfo row{0, 0, 0, 0.0f, 0ull};
-    if (tid < rows) row = scored_row(a, b, kvh, q0 * G + tid, seqlen, n);
+    if (tid < rows) row = scored_row(a, b, q0 * G + tid, in, seqlen, n);
     sRow[tid] = row;
     const bool some = row.lo < row.hi;
     const int lo0 = __reduce_min_sync(0xffffffffu, some ? row.lo : 0x7fffffff);
@@ -177,33 +170,43 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     const int lo1 = __reduce_max_sync(0xffffffffu, some ? row.lo : 0);
     const int hi0 = __reduce_min_sync(0xffffffffu, some ? (tree ? min(base, row.hi) : row.hi) : 0x7fffffff);
     if (lane == 0) s_red[warp][0] = lo0, s_red[warp][1] = hi1, s_red[warp][2] = lo1, s_red[warp][3] = hi0;
-  }
-  // ---- Q to shared memory: fp16 (bf16 is converted, exact within fp16's range) ----
-  // Four loads in flight per thread (the rows' latency is the start of the CTA).
-  for (int p0 = tid; p0 < M * (D / 8); p0 += 4 * C::THREADS) {
-    uint4 v[4];
+  } else {
+    if (tid < M + 64) scored_depths(a, b, n, tid - M, s_depth);
+    // Q to shared memory as fp16 (bf16 is converted, exact within fp16's
+    // range), eight loads in flight per thread.
+    constexpr int QTHR = C::THREADS - M;
+    for (int p0 = tid - M; p0 < M * (D / 8); p0 += 8 * QTHR) {
+      uint4 v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int piece = p0 + i * C::THREADS, r = piece / (D / 8), k0 = (piece % (D / 8)) * 8;
-      v[i] = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        const int64_t qrow = ((int64_t)b * a.n_q + q0 + r / G) * a.n_q_heads + kvh * G + r % G;
-        v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + qrow * D + k0));
+      for (int i = 0; i < 8; ++i) {
+        const int piece = p0 + i * QTHR, r = piece / (D / 8), k0 = (piece % (D / 8)) * 8;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (r < rows) {
+          const int64_t qrow = ((int64_t)b * a.n_q + q0 + r / G) * a.n_q_heads + kvh * G + r % G;
+          v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + qrow * D + k0));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int piece = p0 + i * QTHR, r = piece / (D / 8), k0 = (piece % (D / 8)) * 8;
+        if (a.q_bf16) {
+          uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
+            w[e] = pack_half2(__low2float(x), __high2float(x));
+          }
+          v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (r < M) *reinterpret_cast<uint4*>(sQ + sw128_offset(r, k0, M)) = v[i];
       }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int piece = p0 + i * C::THREADS, r = piece / (D / 8), k0 = (piece % (D / 8)) * 8;
-      if (a.q_bf16) {
-        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
-          w[e] = pack_half2(__low2float(x), __high2float(x));
-        }
-        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      if (r < M) *reinterpret_cast<uint4*>(sQ + sw128_offset(r, k0, M)) = v[i];
+    constexpr float inv = 1.0f / centroid_scale(B);
+    for (int e = tid - M; e < C::LUT * 32; e += QTHR) {
+      const int f = e >> 5;
+      const int klo = (B == 4) ? f : (f & ((1 << B) - 1));
+      const int khi = (B == 4) ? f : (f >> B);
+      sLut[e] = pack_half2(tbq_centroid<B>(klo) * inv, tbq_centroid<B>(khi) * inv);
     }
   }
   // P' of the row groups without a real row stays zero.
@@ -294,37 +297,43 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
 #pragma unroll
       for (int r = 0; r < KR; ++r) w4[r] = kw[r], sc[r] = ks[r];
       fetch_k(step_n, c_n);
-      slot_wait(g);
-      slot_wait(g + 1);
-      uint8_t* const s_hi = ring + g % NSLOT * C::SLOT + k_dst;
-      uint8_t* const s_lo = ring + (g + 1) % NSLOT * C::SLOT + k_dst;
+      // Both slots at once; with three slots in all, hi is handed over first and
+      // lo formed after it, so that the other team's chunk can start.
+      constexpr int PASSES = NSLOT < 4 ? 2 : 1;
 #pragma unroll
-      for (int r = 0; r < KR; ++r) {
-        const uint32_t w[4] = {w4[r].x, w4[r].y, w4[r].z, w4[r].w};
+      for (int pass = 0; pass < PASSES; ++pass) {
+        slot_wait(g + pass);
+        if constexpr (PASSES == 1) slot_wait(g + 1);
+        uint8_t* const s_hi = ring + (g + pass) % NSLOT * C::SLOT + k_dst;
+        uint8_t* const s_lo = ring + (g + 1) % NSLOT * C::SLOT + k_dst;
 #pragma unroll
-        for (int hs = 0; hs < 2; ++hs) {
-          const uint32_t dd = __byte_perm(sc[r], 0u, hs ? 0x3232 : 0x1010);
-          const __half2 d2 = *reinterpret_cast<const __half2*>(&dd);
-          uint32_t qh[4], hi[4], lo[4];
-          i8x4_to_half2x2(w[2 * hs], qh[0], qh[1]);
-          i8x4_to_half2x2(w[2 * hs + 1], qh[2], qh[3]);
+        for (int r = 0; r < KR; ++r) {
+          const uint32_t w[4] = {w4[r].x, w4[r].y, w4[r].z, w4[r].w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __half2 qv = *reinterpret_cast<const __half2*>(&qh[e]);
-            const __half2 h = __hmul2(qv, d2);
-            const __half2 l = __hfma2(qv, d2, __hneg2(h));
-            hi[e] = *reinterpret_cast<const uint32_t*>(&h);
-            lo[e] = *reinterpret_cast<const uint32_t*>(&l);
+          for (int hs = 0; hs < 2; ++hs) {
+            const uint32_t dd = __byte_perm(sc[r], 0u, hs ? 0x3232 : 0x1010);
+            const __half2 d2 = *reinterpret_cast<const __half2*>(&dd);
+            uint32_t qh[4], hi[4], lo[4];
+            i8x4_to_half2x2(w[2 * hs], qh[0], qh[1]);
+            i8x4_to_half2x2(w[2 * hs + 1], qh[2], qh[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const __half2 qv = *reinterpret_cast<const __half2*>(&qh[e]);
+              const __half2 h = __hmul2(qv, d2);
+              const __half2 l = __hfma2(qv, d2, __hneg2(h));
+              hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+              lo[e] = *reinterpret_cast<const uint32_t*>(&l);
+            }
+            const int row = (r * KS * kTile + 8 * hs) * 128;
+            if (pass == 0) *reinterpret_cast<uint4*>(s_hi + row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if (pass == 1 || PASSES == 1) *reinterpret_cast<uint4*>(s_lo + row) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
-          const int row = (r * KS * kTile + 8 * hs) * 128;
-          *reinterpret_cast<uint4*>(s_hi + row) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(s_lo + row) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
+        fence_proxy_async();
+        __syncwarp();
+        slot_done(g + pass);
+        if constexpr (PASSES == 1) slot_done(g + 1);
       }
-      fence_proxy_async();
-      __syncwarp();
-      slot_done(g);
-      slot_done(g + 1);
     };
     // V chunk c of a step: units of (lane stream, 8 dims), 16 fields of 2B
     // bits in B words of the stream. Unit v = 16 part + 4 record + (stream % 4),
@@ -783,19 +792,31 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
       }
     }
     named_bar(5, C::SOFT);
-    for (int r = r0 + warp; r < min(rows, r0 + C::RP); r += C::SOFT / 32) {
-      float2 v[D / 64];
+    // A warp takes RPW rows together: a row alone is a chain of shuffles.
+    constexpr int RPW = D == 512 ? 1 : D == 256 ? 2 : 4, WARPS = C::SOFT / 32;
+    for (int rw = r0 + RPW * warp; rw < min(rows, r0 + C::RP); rw += RPW * WARPS) {
+      float2 v[RPW][D / 64];
 #pragma unroll
-      for (int e = 0; e < D / 64; ++e)
-        v[e] = *reinterpret_cast<const float2*>(stage + (r - r0) * C::STRIDE + 64 * e + 2 * lane);
-      if (direct) {
+      for (int k = 0; k < RPW; ++k)
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e)
+          v[k][e] = *reinterpret_cast<const float2*>(stage + (rw + k - r0) * C::STRIDE + 64 * e + 2 * lane);
+      float* o[RPW];
+#pragma unroll
+      for (int k = 0; k < RPW; ++k) {
+        const int r = rw + k;
         const int64_t orow = ((int64_t)b * a.n_q + q0 + r / G) * a.n_q_heads + kvh * G + r % G;
-        float* const o = a.out_type == kOutF32 ? a.out + orow * D
-                                               : reinterpret_cast<float*>(reinterpret_cast<uint16_t*>(a.out) + orow * D);
-        derotate_store_row<D, ROT, true>(v, lane, a.signs, o, centroid_scale(B), a.signs2, a.out_type);
-      } else {
-        derotate_store_row<D>(v, lane, nullptr, slot + (int64_t)r * D);
+        float* const to = !direct                   ? slot + (int64_t)r * D
+                          : a.out_type == kOutF32 ? a.out + orow * D
+                                                  : reinterpret_cast<float*>(reinterpret_cast<uint16_t*>(a.out) + orow * D);
+        o[k] = r < rows ? to : nullptr;
       }
+      if (direct) derotate_rows<D, ROT, RPW>(v, lane, a.signs, centroid_scale(B), a.signs2);
+#pragma unroll
+      for (int k = 0; k < RPW; ++k)
+        if (o[k])
+#pragma unroll
+          for (int e = 0; e < D / 64; ++e) store_out2<true>(o[k], lane + 32 * e, v[k][e], direct ? a.out_type : kOutF32);
     }
     named_bar(5, C::SOFT);
   }

@@ -235,6 +235,53 @@ __device__ __forceinline__ void derotate_store_row(float2 (&v)[D / 64], int lane
   }
 }
 
+// The inverse rotation of derotate_store_row on N rows of a warp at once, in
+// place (the shuffles of the rows overlap).
+template <int D, int ROT, int N>
+__device__ __forceinline__ void derotate_rows(float2 (&v)[N][D / 64], int lane, const int8_t* signs, float vscale,
+                                              const int8_t* signs2) {
+  constexpr int E2 = D / 64;
+  constexpr int EG = ROT ? kRotGroup / 64 : E2;
+  constexpr float GSCALE = ROT ? 1.0f / kRotGroup : 1.0f / D;
+  auto flip = [&](const int8_t* s, float scale) {
+#pragma unroll
+    for (int e = 0; e < E2; ++e) {
+      const char2 sg = *reinterpret_cast<const char2*>(s + 64 * e + 2 * lane);
+      const float fx = sg.x < 0 ? -scale : scale, fy = sg.y < 0 ? -scale : scale;
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k][e] = make_float2(v[k][e].x * fx, v[k][e].y * fy);
+    }
+  };
+  if constexpr (ROT) flip(signs2, 1.0f);
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int e = 0; e < E2; ++e) v[k][e] = make_float2(v[k][e].x + v[k][e].y, v[k][e].x - v[k][e].y);
+#pragma unroll
+  for (int hl = 1; hl < 32; hl <<= 1) {
+    const float s = (lane & hl) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int e = 0; e < E2; ++e) {
+        const float ox = __shfl_xor_sync(0xffffffffu, v[k][e].x, hl), oy = __shfl_xor_sync(0xffffffffu, v[k][e].y, hl);
+        v[k][e] = make_float2(fmaf(s, v[k][e].x, ox), fmaf(s, v[k][e].y, oy));
+      }
+  }
+#pragma unroll
+  for (int hh = 1; hh < EG; hh <<= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int e = 0; e < E2; ++e)
+        if ((e & hh) == 0) {
+          const float2 x0 = v[k][e], x1 = v[k][e + hh];
+          v[k][e] = make_float2(x0.x + x1.x, x0.y + x1.y);
+          v[k][e + hh] = make_float2(x0.x - x1.x, x0.y - x1.y);
+        }
+  flip(signs, vscale * GSCALE);
+}
+
 // CTA epilogue. Merges the NP tile groups' softmax states and accumulators
 // into one partial per row, applies the inverse transform and sign flip (when
 // `signs` is set: the values were accumulated in the rotated basis), and

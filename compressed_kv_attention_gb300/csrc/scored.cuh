@@ -57,40 +57,55 @@ __device__ __forceinline__ void scored_lengths(const ScoredArgs& a, int b, bool 
   }
 }
 
-__device__ __forceinline__ RowInfo scored_row(const ScoredArgs& a, int b, int kvh, int rr, int seqlen, int n) {
+// Everything a row reads from memory, issued at once (beside the lengths).
+struct RowLoads {
+  float slope;
+  int prefix, doc;
+  uint64_t tree;
+};
+__device__ __forceinline__ RowLoads scored_row_loads(const ScoredArgs& a, int b, int kvh, int rr) {
+  const int G = a.n_q_heads / a.n_kv_heads, i = rr / G;
+  RowLoads l{0.0f, 0, 0, 0ull};
+  if (i >= a.n_q) return l;
+  if (a.slopes) l.slope = a.slopes[kvh * G + rr % G] * 1.4426950408889634f;
+  if (a.prefix_len) l.prefix = a.prefix_len[b];
+  if (a.doc_start) l.doc = a.doc_start[(int64_t)b * a.n_q + i];
+  if (a.tree) l.tree = a.tree[(int64_t)b * a.n_q + i];
+  return l;
+}
+
+__device__ __forceinline__ RowInfo scored_row(const ScoredArgs& a, int b, int rr, const RowLoads& in, int seqlen,
+                                              int n) {
   RowInfo r{0, 0, 0, 0.0f, 0ull};
-  const int G = a.n_q_heads / a.n_kv_heads;
-  const int i = rr / G;
+  const int i = rr / (a.n_q_heads / a.n_kv_heads);
   if (i >= n) return r;
-  if (a.slopes) r.slope = a.slopes[kvh * G + rr % G] * 1.4426950408889634f;
+  r.slope = in.slope;
   const int base = seqlen - n;
   int64_t lo = 0;
   if (a.tree) {
-    const uint64_t* masks = a.tree + (int64_t)b * a.n_q;
-    r.tree = masks[i] & low_bits(n);
+    r.tree = in.tree & low_bits(n);
     const int depth = __popcll(r.tree) - 1;
     r.at = base + depth;
     r.hi = seqlen;
     if (a.window) {
       lo = (int64_t)r.at - a.window + 1;
-      if (a.window < 64)  // drafted keys further above than the window (depths differ by 63 at most)
+      if (a.window < 64) {  // drafted keys further above than the window (depths differ by 63 at most)
+        const uint64_t* masks = a.tree + (int64_t)b * a.n_q;
         for (int j = 0; j < n; ++j)
           if ((r.tree >> j & 1ull) && depth - (__popcll(masks[j] & low_bits(n)) - 1) >= a.window)
             r.tree &= ~(1ull << j);
+      }
     }
+    // The interval bounds the committed keys only: the drafted ones are the bits.
+    lo = min(lo, (int64_t)base);
   } else {
     r.at = base + i;
     if (r.at < 0) return RowInfo{0, 0, 0, 0.0f, 0ull};
     r.hi = r.at + 1;
-    if (a.prefix_len) {
-      const int p = a.prefix_len[b];
-      r.hi = max(r.hi, min(p, seqlen));
-    }
+    if (a.prefix_len) r.hi = max(r.hi, min(in.prefix, seqlen));
     if (a.window) lo = (int64_t)r.at - a.window + 1;
-    if (a.doc_start) lo = max(lo, (int64_t)a.doc_start[(int64_t)b * a.n_q + i]);
+    if (a.doc_start) lo = max(lo, (int64_t)in.doc);
   }
-  // A tree's interval bounds the committed keys only: the drafted ones are its bits.
-  if (a.tree) lo = min(lo, (int64_t)base);
   r.lo = static_cast<int>(min(max(lo, (int64_t)0), (int64_t)r.hi));
   if (r.lo >= r.hi || (a.tree && r.lo == base && r.tree == 0ull)) r.lo = r.hi = 0;
   return r;
