@@ -73,7 +73,8 @@ struct CTiles {
   static constexpr int TEAM = WIDEN / 2;
   static constexpr int THREADS = SOFT + WIDEN + 128;  // the MMA warp, in a warpgroup of its own
   // Registers per thread of the roles: 5 warpgroups are launched with 96 each.
-  static constexpr int REG_SOFT = D == 512 ? 152 : 136, REG_WIDEN = D == 512 ? 72 : 88, REG_MMA = 32;
+  static constexpr bool WIDE = D == 512 && !ROT;     // the tail dims want registers, the rotated widening more
+  static constexpr int REG_SOFT = WIDE ? 152 : 136, REG_WIDEN = WIDE ? 72 : 88, REG_MMA = 32;
   static_assert(2 * REG_SOFT + 2 * REG_WIDEN + REG_MMA <= 5 * 96, "the roles share the launch's registers");
   // Output staging of the epilogue: RP rows at a time, padded by 16 bytes.
   static constexpr int STRIDE = D + 4;

@@ -953,7 +953,7 @@ static ckv_status plan_scored(const ckv_cache* cache, int64_t max_seq_len, int n
     sp->ws = 256 + (ns == 1 ? 0 : static_cast<size_t>(units) * ns * 128 * (cache->head_dim + 1) * row);
     return CKV_OK;
   }
-  sp->n_split = n_split ? n_split : auto_split(p.groups, keys, cache->head_dim == 512 ? 4 : 8, cache->head_dim <= 128 ? 2 : 1);
+  sp->n_split = n_split ? n_split : auto_split(p.groups, keys, cache->head_dim == 512 ? 6 : 8, cache->head_dim <= 128 ? 2 : 1);
   sp->part = ws_header_bytes(p.groups, sp->n_split);
   sp->ws = sp->n_split == 1 ? sp->part : decode_ws_bytes(cache->head_dim, p.groups, sp->n_split);
   return CKV_OK;
