@@ -275,6 +275,12 @@ __global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, CScored<D, B, ROT
     for (int e = 0; e < 4; ++e) S[e] = Sn[e];
   }
 
+  // After a wait that ran out copies may still be landing: give each its bounded
+  // wait before the memory is used again.
+  if (leader && *(volatile int*)&s_abort)
+    for (int k = n_iters > C::NSTAGE ? n_iters - C::NSTAGE : 0; k < n_iters; ++k)
+      mbar_wait(&full[k % C::NSTAGE], (k / C::NSTAGE) & 1);
+
   // Rows that see nothing took part in the tiles that every other row sees
   // whole: they leave as empty rows.
   const bool e0 = s_row[2 * t].hi == 0, e1 = s_row[2 * t + 1].hi == 0;

@@ -73,8 +73,7 @@ struct CTiles {
   static constexpr int TEAM = WIDEN / 2;
   static constexpr int THREADS = SOFT + WIDEN + 128;  // the MMA warp, in a warpgroup of its own
   // Registers per thread of the roles: 5 warpgroups are launched with 96 each.
-  static constexpr bool WIDE = D == 512 && !ROT;     // the tail dims want registers, the rotated widening more
-  static constexpr int REG_SOFT = WIDE ? 152 : 136, REG_WIDEN = WIDE ? 72 : 88, REG_MMA = 32;
+  static constexpr int REG_SOFT = 136, REG_WIDEN = 88, REG_MMA = 32;
   static_assert(2 * REG_SOFT + 2 * REG_WIDEN + REG_MMA <= 5 * 96, "the roles share the launch's registers");
   // Output staging of the epilogue: RP rows at a time, padded by 16 bytes.
   static constexpr int STRIDE = D + 4;
@@ -272,7 +271,7 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     const int k_sc = k_rec * C::REC + k_scale_offset(D) + 2 * (kpp * C::NB + k_blk);
     const uint32_t k_dst = sw128_offset(k_rec * kTile + kpp, k_blk * 32 + 8 * kq, NKV);  // + 128 per row
     uint4 kw[KR];
-    uint32_t ks[KR];  // the two tokens' scales
+    uint16_t ks[KR][2];  // the two tokens' scales, as loaded: an operation on them at the fetch would wait for them there
     auto fetch_k = [&](int step, int c) {
       const uint8_t* p = step_base(step);
       const int recs = step_recs(step);
@@ -282,11 +281,11 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
           const int at = r * KS * C::REC;
           kw[r] = *reinterpret_cast<const uint4*>(p + k_src + at + c * (NBLK * 512));
           const uint8_t* sc = p + k_sc + at + c * (NBLK * 2);
-          ks[r] = *reinterpret_cast<const uint16_t*>(sc) |
-                  (uint32_t)*reinterpret_cast<const uint16_t*>(sc + 16 * C::NB) << 16;
+          ks[r][0] = *reinterpret_cast<const uint16_t*>(sc);
+          ks[r][1] = *reinterpret_cast<const uint16_t*>(sc + 16 * C::NB);
         } else {
           kw[r] = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);
-          ks[r] = 0u;
+          ks[r][0] = ks[r][1] = 0;
         }
       }
     };
@@ -294,9 +293,9 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     auto widen_k = [&](int step, int c, int step_n, int c_n) {
       const int g = k_index(step, c);
       uint4 w4[KR];
-      uint32_t sc[KR];
+      uint16_t sc[KR][2];
 #pragma unroll
-      for (int r = 0; r < KR; ++r) w4[r] = kw[r], sc[r] = ks[r];
+      for (int r = 0; r < KR; ++r) w4[r] = kw[r], sc[r][0] = ks[r][0], sc[r][1] = ks[r][1];
       fetch_k(step_n, c_n);
       // Both slots at once; with three slots in all, hi is handed over first and
       // lo formed after it, so that the other team's chunk can start.
@@ -312,8 +311,7 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
           const uint32_t w[4] = {w4[r].x, w4[r].y, w4[r].z, w4[r].w};
 #pragma unroll
           for (int hs = 0; hs < 2; ++hs) {
-            const uint32_t dd = __byte_perm(sc[r], 0u, hs ? 0x3232 : 0x1010);
-            const __half2 d2 = *reinterpret_cast<const __half2*>(&dd);
+            const __half2 d2 = __half2half2(__ushort_as_half(sc[r][hs]));
             uint32_t qh[4], hi[4], lo[4];
             i8x4_to_half2x2(w[2 * hs], qh[0], qh[1]);
             i8x4_to_half2x2(w[2 * hs + 1], qh[2], qh[3]);
@@ -562,10 +560,11 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     float* const norms = sNorm + (warp & 3) * 2 * NKV;
     const uint8_t* const nbase = stream + (int64_t)s0 * (4 * C::REC) + nk / kTile * C::REC + v_norm_offset(D, B) + 2 * (nk % kTile);
     const int nkeys = seqlen - s0 * NKV - nk;  // step i has this key where 64 i < nkeys
-    auto load_norm = [&](int step) {
+    // As loaded: an operation on the value here would wait for it here.
+    auto load_norm = [&](int step) -> uint16_t {
       return (!ROT && step < n_steps && step * NKV < nkeys)
-                 ? __half2float(*reinterpret_cast<const __half*>(nbase + (int64_t)step * (4 * C::REC)))
-                 : 0.0f;
+                 ? *reinterpret_cast<const uint16_t*>(nbase + (int64_t)step * (4 * C::REC))
+                 : (uint16_t)0;
     };
     // The last output dims of a step's P' C: 64 part .. of them, 32 per thread.
     auto add_tail = [&](int step, int part) {
@@ -588,11 +587,11 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
                                                                                                  : kFormPlain;
     const float zA = form == kFormAny ? 1.0f : form == kFormCap ? -2.0f * a.cap_log2 : a.mul;
     const float zC = form == kFormCap ? a.cap_log2 : 0.0f;
-    float nrm = load_norm(0);
+    uint16_t nrm = load_norm(0);
     for (int i = 0; i < n_steps; ++i) {
       const int buf = i % NS;
       if constexpr (!ROT) {
-        norms[(i & 1) * NKV + nk] = nrm;
+        norms[(i & 1) * NKV + nk] = __half2float(__ushort_as_half(nrm));
         nrm = load_norm(i + 1);
       }
       if (i > 0) {  // at once: S of the next step waits for these columns

@@ -141,6 +141,48 @@ def test_split_counts_and_both_merges(n_split):
     assert torch.equal(want[0], again[0]) and torch.equal(want[1], again[1])  # no order depends on timing
 
 
+@pytest.mark.parametrize("n_split", [0, 1, 2, 7, 11, 40, 200])
+@pytest.mark.parametrize("D,rot", [(64, False), (128, True), (512, False), (512, True)])
+def test_tiles_at_every_split_count(D, rot, n_split):
+    """More than 32 query rows per kv head (the tiles), shares with and without keys, both merges of the partials."""
+    lens, n_of = [700, 0, 41, 320], [20, 5, 20, 3]
+    c = Cache(D, 2, [max(1, t) for t in lens], 704, rot=rot)
+    q = queries(4, 20, 12, D, 4)
+    kw = dict(cap=12.0, alibi=D == 128, n_split=n_split, n_of=n_of, window=300)
+    want = compare(c, lens, q, f"tiles {D} {n_split}", **kw)
+    again = run(c, lens, q, **kw)
+    assert torch.equal(want[0], again[0]) and torch.equal(want[1], again[1])
+    for out_type in (torch.float16, torch.bfloat16):
+        compare(c, lens, q, f"tiles {D} {n_split} {out_type}", out_type=out_type, **kw)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 512])
+def test_prompts_of_several_tiles(D):
+    """A whole prompt and the last chunk of one: query tiles that end inside a document, a prefix, an odd last tile."""
+    T = 333
+    c = Cache(D, 1, [T, 290], 336, seed=D)
+    starts = np.array([0, 37, 38, 129, 250])
+    for n_q, Hq in ((290, 8), (131, 3)):
+        q = queries(2, n_q, Hq, D, n_q, torch.bfloat16)
+        doc = [starts[np.searchsorted(starts, np.arange(t - n_q, t), side="right") - 1] for t in (T, 290)]
+        for kw in (dict(doc=doc), dict(prefix=[200, 290], cap=30.0), dict(window=65, alibi=True, doc=doc)):
+            compare(c, [T, 290], q, f"prompt {D} {n_q} {list(kw)}", out_type=torch.bfloat16, **kw)
+
+
+def test_probabilities_after_the_largest_logit_moves():
+    """Keys whose logits climb along the sequence: the running maximum and the accumulated rows are rescaled often."""
+    for D, n_q in ((128, 1), (128, 24), (512, 12)):
+        c = Cache(D, 1, [640], 640, seed=9)
+        q = queries(1, n_q, 4, D, 3)
+        c.k[0] *= np.linspace(0.1, 6.0, 640)[None, :, None]
+        k = torch.from_numpy(c.k[0].transpose(1, 0, 2)[None].astype(np.float16)).to(DEV)
+        v = inputs.normal_tensor((1, 640, 1, D), 9, "v", np.zeros(0, np.int64))
+        ckv.kv_pack(c.packed, 0, k.contiguous(), torch.from_numpy(v).to(DEV))
+        c.read()
+        compare(c, [640], q, f"climbing {D} {n_q}")
+        compare(c, [640], q, f"climbing {D} {n_q}", alibi=True, n_split=3)
+
+
 @pytest.mark.parametrize("rot", [False, True])
 def test_unwritten_positions_and_left_padding(rot):
     """Positions before the padding's end and after the length are NaN bytes and must not be seen."""
@@ -211,7 +253,7 @@ def test_types(q_type, out_type):
                     n_split=n_split, cap=25.0)
 
 
-@pytest.mark.parametrize("Hkv,Hq", [(1, 1), (3, 3), (2, 14), (1, 40), (8, 8)])
+@pytest.mark.parametrize("Hkv,Hq", [(1, 1), (3, 3), (2, 14), (1, 40), (8, 8), (1, 128), (1, 136)])
 def test_head_ratios(Hkv, Hq):
     c = Cache(64, Hkv, [129, 50], 144)
     for n_q in (1, 2, 11):
