@@ -631,7 +631,7 @@ CKV_API ckv_status ckv_attn_scored(const ckv_cache* cache, const int32_t* seq_le
                                    void* stream);
 
 /*
- * attn_tree — attn_verify for a tree of drafted tokens: the n nodes (n_q, or
+ * attn_tree — attn_decode_verify for a tree of drafted tokens: the n nodes (n_q, or
  * q_len[b]) are the newest n positions of the sequence (their K and V rows
  * packed, their lengths counted), base = seq_len[b] - n. Node t sees every
  * position below base and node j where bit j of tree_mask[b][t] is set (its
