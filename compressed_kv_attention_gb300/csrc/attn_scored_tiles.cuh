@@ -173,22 +173,26 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
   } else {
     if (tid < M + 64) scored_depths(a, b, n, tid - M, s_depth);
     // Q to shared memory as fp16 (bf16 is converted, exact within fp16's
-    // range), eight loads in flight per thread.
-    constexpr int QTHR = C::THREADS - M;
-    for (int p0 = tid - M; p0 < M * (D / 8); p0 += 8 * QTHR) {
-      uint4 v[8];
+    // range), four loads in flight per thread. The splits of a tile load the same
+    // rows at once: each starts at its own place.
+    constexpr int QTHR = C::THREADS - M, PIECES = M * (D / 8);
+    const int turn0 = static_cast<int>(blockIdx.x * 37u % 64u) * (PIECES / 64);
+#pragma unroll 1
+    for (int p0 = tid - M; p0 < PIECES; p0 += 4 * QTHR) {
+      uint4 v[4];
+      int at[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int piece = p0 + i * QTHR, r = piece / (D / 8), k0 = (piece % (D / 8)) * 8;
+      for (int i = 0; i < 4; ++i) {
+        const int piece = (p0 + i * QTHR + turn0) % PIECES, r = piece / (D / 8), k0 = (piece % (D / 8)) * 8;
+        at[i] = p0 + i * QTHR < PIECES ? static_cast<int>(sw128_offset(r, k0, M)) : -1;
         v[i] = make_uint4(0, 0, 0, 0);
-        if (r < rows) {
+        if (r < rows && at[i] >= 0) {
           const int64_t qrow = ((int64_t)b * a.n_q + q0 + r / G) * a.n_q_heads + kvh * G + r % G;
           v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + qrow * D + k0));
         }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int piece = p0 + i * QTHR, r = piece / (D / 8), k0 = (piece % (D / 8)) * 8;
+      for (int i = 0; i < 4; ++i) {
         if (a.q_bf16) {
           uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
@@ -198,10 +202,11 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
           }
           v[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (r < M) *reinterpret_cast<uint4*>(sQ + sw128_offset(r, k0, M)) = v[i];
+        if (at[i] >= 0) *reinterpret_cast<uint4*>(sQ + at[i]) = v[i];
       }
     }
     constexpr float inv = 1.0f / centroid_scale(B);
+#pragma unroll 1
     for (int e = tid - M; e < C::LUT * 32; e += QTHR) {
       const int f = e >> 5;
       const int klo = (B == 4) ? f : (f & ((1 << B) - 1));
@@ -477,26 +482,23 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
       if (elect_one()) umma_commit(&b_free[slot]);
       if (++slot == NSLOT) slot = 0, turn ^= 1u;
     };
+    // (Rolled over the chunks: code that runs once per tile is paid for by the
+    // instruction fetch, and the three roles' loops share the cache.)
     auto s_step = [&](int i) {
       const int buf = i % NS;
       if (i >= NS) wait(&b_sfree[buf], i / NS - 1);
+#pragma unroll 1
+      for (int c = 0; c < 2 * NCH; ++c) {  // chunk c / 2, hi then lo
+        wait(&b_full[slot], turn);
+        tc_fence_after();
+        const uint32_t s_lo = r_lo + slot * (C::SLOT >> 4), a_lo = q_lo + (c >> 1) * ((CW / 64) * (M * 128) >> 4);
+        if (elect_one()) {
 #pragma unroll
-      for (int c = 0; c < NCH; ++c) {
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {  // hi, lo
-          wait(&b_full[slot], turn);
-          tc_fence_after();
-          const uint32_t s_lo = r_lo + slot * (C::SLOT >> 4);
-          if (elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < CW / 16; ++ks) {
-              const int kd = c * (CW / 16) + ks;
-              umma_f16_lo(tmem + 64 * buf, q_lo + (((kd >> 2) * (M * 128) + (kd & 3) * 32) >> 4),
-                          s_lo + (((ks >> 2) * (NKV * 128) + (ks & 3) * 32) >> 4), kS, c > 0 || part > 0 || ks > 0);
-            }
-          }
-          slot_next();
+          for (int ks = 0; ks < CW / 16; ++ks)
+            umma_f16_lo(tmem + 64 * buf, a_lo + (((ks >> 2) * (M * 128) + (ks & 3) * 32) >> 4),
+                        s_lo + (((ks >> 2) * (NKV * 128) + (ks & 3) * 32) >> 4), kS, c > 0 || ks > 0);
         }
+        slot_next();
       }
       if (elect_one()) umma_commit(&b_sfull[buf]);
     };
