@@ -418,7 +418,7 @@ def _cache_device(cache) -> int:
     return dev
 
 
-def _scored_tensors(cache, seq_len, q, out, lse, workspace, q_len, slopes):
+def _scored_tensors(cache, seq_len, q, out, lse, workspace, q_len, slopes, window):
     import torch
     dev, shape, f32, i32 = _cache_device(cache), q.shape, (torch.float32,), (torch.int32,)
     if len(shape) != 4 or shape[0] != cache.batch or shape[3] != cache.head_dim:
@@ -432,6 +432,8 @@ def _scored_tensors(cache, seq_len, q, out, lse, workspace, q_len, slopes):
         _expect(q_len, "q_len", shape[:1], i32, dev)
     if slopes is not None:
         _expect(slopes, "slopes", shape[2:3], f32, dev)
+    if window >> 31:  # ctypes would cut it to 32 bits
+        raise ValueError(f"window must be in [0, 2**31), got {window}")
     return dev, shape
 
 
@@ -447,7 +449,7 @@ def attn_scored(cache: PackedCache, seq_len, max_seq_len: int, q, scale: float, 
     [batch]) and a document mask (doc_start int32 [batch, n_q]). q: fp16 or bf16 [batch, n_q, n_q_heads, D];
     out: float32, fp16 or bf16 like q; lse float32 [batch, n_q, n_q_heads]."""
     import torch
-    dev, shape = _scored_tensors(cache, seq_len, q, out, lse, workspace, q_len, slopes)
+    dev, shape = _scored_tensors(cache, seq_len, q, out, lse, workspace, q_len, slopes, window)
     if prefix_len is not None:
         _expect(prefix_len, "prefix_len", shape[:1], (torch.int32,), dev)
     if doc_start is not None:
@@ -470,7 +472,7 @@ def attn_tree(cache: PackedCache, seq_len, max_seq_len: int, tree_mask, q, scale
     sees the committed cache and the nodes whose bits are set in tree_mask[b, t] (int64 or uint64 [batch, n_q],
     its ancestors and itself). Tensors as attn_scored."""
     import torch
-    dev, shape = _scored_tensors(cache, seq_len, q, out, lse, workspace, q_len, slopes)
+    dev, shape = _scored_tensors(cache, seq_len, q, out, lse, workspace, q_len, slopes, window)
     _expect(tree_mask, "tree_mask", shape[:2], (torch.int64, torch.uint64), dev)
     score = CkvScoreStruct(softcap, window, _ptr(slopes), None, None)
     codes = _dtypes()

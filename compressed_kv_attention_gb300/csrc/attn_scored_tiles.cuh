@@ -172,39 +172,29 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
     if (lane == 0) s_red[warp][0] = lo0, s_red[warp][1] = hi1, s_red[warp][2] = lo1, s_red[warp][3] = hi0;
   } else {
     if (tid < M + 64) scored_depths(a, b, n, tid - M, s_depth);
-    // Q to shared memory as fp16 (bf16 is converted, exact within fp16's
-    // range), four loads in flight per thread. The splits of a tile load the same
-    // rows at once: each starts at its own place.
+    // Q to shared memory by asynchronous copies, all of a thread's in flight at
+    // once. The splits of a tile load the same rows together: each starts at its
+    // own place.
     constexpr int QTHR = C::THREADS - M, PIECES = M * (D / 8);
     const int turn0 = static_cast<int>(blockIdx.x * 37u % 64u) * (PIECES / 64);
-#pragma unroll 1
-    for (int p0 = tid - M; p0 < PIECES; p0 += 4 * QTHR) {
-      uint4 v[4];
-      int at[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int piece = (p0 + i * QTHR + turn0) % PIECES, r = piece / (D / 8), k0 = (piece % (D / 8)) * 8;
-        at[i] = p0 + i * QTHR < PIECES ? static_cast<int>(sw128_offset(r, k0, M)) : -1;
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (r < rows && at[i] >= 0) {
-          const int64_t qrow = ((int64_t)b * a.n_q + q0 + r / G) * a.n_q_heads + kvh * G + r % G;
-          v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + qrow * D + k0));
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (a.q_bf16) {
-          uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
-            w[e] = pack_half2(__low2float(x), __high2float(x));
-          }
-          v[i] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        if (at[i] >= 0) *reinterpret_cast<uint4*>(sQ + at[i]) = v[i];
+    auto q_piece = [&](int p, int& r, int& k0) {
+      const int piece = (p + turn0) % PIECES;
+      r = piece / (D / 8);
+      k0 = (piece % (D / 8)) * 8;
+      return smem_u32(sQ) + sw128_offset(r, k0, M);
+    };
+#pragma unroll 4
+    for (int p = tid - M; p < PIECES; p += QTHR) {
+      int r, k0;
+      const uint32_t dst = q_piece(p, r, k0);
+      if (r < rows) {
+        const __half* src = a.q + (((int64_t)b * a.n_q + q0 + r / G) * a.n_q_heads + kvh * G + r % G) * D + k0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+      } else {
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0u) : "memory");
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
     constexpr float inv = 1.0f / centroid_scale(B);
 #pragma unroll 1
     for (int e = tid - M; e < C::LUT * 32; e += QTHR) {
@@ -212,6 +202,23 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
       const int klo = (B == 4) ? f : (f & ((1 << B) - 1));
       const int khi = (B == 4) ? f : (f >> B);
       sLut[e] = pack_half2(tbq_centroid<B>(klo) * inv, tbq_centroid<B>(khi) * inv);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (a.q_bf16) {  // to fp16 in place, each thread its own copies (exact within fp16's range)
+#pragma unroll 4
+      for (int p = tid - M; p < PIECES; p += QTHR) {
+        int r, k0;
+        const uint32_t dst = q_piece(p, r, k0);
+        const uint4 v = lds128(dst);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
+          w[e] = pack_half2(__low2float(x), __high2float(x));
+        }
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                     : "memory");
+      }
     }
   }
   // P' of the row groups without a real row stays zero.

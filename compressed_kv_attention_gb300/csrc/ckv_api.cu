@@ -935,6 +935,8 @@ static ckv_status plan_scored(const ckv_cache* cache, int64_t max_seq_len, int n
   if (s != CKV_OK) return s;
   const int64_t bh = static_cast<int64_t>(cache->batch) * cache->n_kv_heads;
   if (bh > 65535) return fail(CKV_ERR_UNSUPPORTED, "batch * n_kv_heads above 65535");
+  if (static_cast<int64_t>(cache->batch) * n_q > 0x7fffffffLL / n_q_heads)
+    return fail(CKV_ERR_UNSUPPORTED, "more than 2^31 - 1 query rows");
   const int G = n_q_heads / cache->n_kv_heads;
   const size_t row = sizeof(float);
   sp->tiles = static_cast<int64_t>(G) * n_q > kTileRows && G <= 128;

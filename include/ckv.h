@@ -614,13 +614,15 @@ typedef struct {
  * out_type (any ckv_dtype), 16-byte aligned; lse float32 [batch][n_q][n_q_heads].
  * n_split: 0 automatic, > 0 that many key splits.
  * Workspace: ckv_attn_scored_workspace bytes (the same n_split), zero-filled
- * once; one call at a time uses it, captured graphs included. A seq_len outside
+ * before its first use, and again before a call of other sizes (batch, heads,
+ * n_q, n_split, max_seq_len, window) uses it: the header's extent goes by them.
+ * One call at a time uses it, captured graphs included. A seq_len outside
  * [0, min(capacity, max_seq_len)] or a q_len outside [0, n_q] makes every row
  * of that sequence empty and raises the device flag (2).
  * Errors: INVALID_ARG (null or misaligned pointers, types, a softcap that is
  * negative or not finite, a negative window, a scale that is not finite),
- * UNSUPPORTED (head dim, head ratio, more than 65535 (sequence, kv head) pairs
- * or 524280 query rows per kv head), WORKSPACE.
+ * UNSUPPORTED (head dim, head ratio, more than 65535 (sequence, kv head) pairs,
+ * 524280 query rows per kv head or 2^31 - 1 query rows in all), WORKSPACE.
  */
 CKV_API size_t ckv_attn_scored_workspace(const ckv_cache* cache, int64_t max_seq_len, int32_t n_q,
                                          int32_t n_q_heads, int32_t n_split);

@@ -280,6 +280,13 @@ def test_wrong_tensors_are_refused():
     bad = [dict(q=q.float()), dict(q=q.transpose(1, 2)), dict(out=out[:, :2]), dict(lse=lse.half()),
            dict(seq_len=sl.long()), dict(slopes=slopes_of(4)), dict(doc_start=ints([[0, 0]])),
            dict(prefix_len=ints([1, 2])), dict(q_len=ints([[3]]))]
+    for window in (-1, 2 ** 31, 2 ** 32 + 5):
+        with pytest.raises(ValueError):
+            ckv.attn_scored(c.packed, sl, 40, q, 0.1, out, lse, ws, window=window)
+    with pytest.raises(ValueError):
+        ckv.attn_scored(c.packed, sl.cpu(), 40, q, 0.1, out, lse, ws)
+    with pytest.raises(ValueError):
+        ckv.tree_accept(c.packed, sl, 3, ints([[0, 1]]), ints([2]).cpu(), ints([0]))
     for kw in bad:
         a = dict(seq_len=sl, q=q, out=out, lse=lse, slopes=None, doc_start=None, prefix_len=None, q_len=None)
         a.update(kw)

@@ -50,7 +50,7 @@ def test_attention_refusals(lib, tree):
         (-1, dict(ns=-1)), (-1, dict(ns=1025)), (-2, dict(hq=7)), (-1, dict(hq=0)),
         (-3, dict(ws=None)), (-3, dict(ws=FAKE + 16)), (-3, dict(wsb=255)),
         (-2, dict(c=cache(D=96))), (-1, dict(c=cache(cap=250))), (-1, dict(c=cache(v_bits=5))),
-        (-2, dict(c=cache(Hkv=2, batch=32768))),
+        (-2, dict(c=cache(Hkv=2, batch=32768))), (-2, dict(c=cache(Hkv=1, batch=60000), nq=64, hq=600)),
     ]:
         assert attend(lib, tree, **kw) == status, kw
         assert lib.ckv_last_error()
