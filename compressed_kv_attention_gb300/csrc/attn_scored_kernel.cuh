@@ -195,7 +195,8 @@ __global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, CScored<D, B, ROT
       const int64_t tpos = tile * kTile;
       // Visibility: position tpos + g is bit g of its row's word, tpos + g + 8 bit g + 8.
       uint32_t v0 = 0xffffu, v1 = 0xffffu, any = 0xffffu;
-      if (tpos < flo || tpos + kTile > fhi) {
+      const bool mixed = tpos < flo || tpos + kTile > fhi;
+      if (mixed) {
         const uint32_t bits = scored_tile_bits(mine, tree, base, tpos);
         v0 = __shfl_sync(0xffffffffu, bits, 2 * t);
         v1 = __shfl_sync(0xffffffffu, bits, 2 * t + 1);
@@ -247,6 +248,19 @@ __global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, CScored<D, B, ROT
         const uint32_t ma = any >> (2 * t), mb = any >> (2 * t + 8);
         nA = lds32(nb) & ((ma & 1u ? 0xffffu : 0u) | (ma & 2u ? 0xffff0000u : 0u));
         nB = lds32(nb + 16) & ((mb & 1u ? 0xffffu : 0u) | (mb & 2u ? 0xffff0000u : 0u));
+        if (mixed) {  // bits as in v0 and v1, over all groups (the lanes of a warp hold them all)
+          const uint32_t bad =
+              __reduce_or_sync(0xffffffffu, bad_norms(nA) << (2 * t) | bad_norms(nB) << (2 * t + 8));
+          if (bad) {
+            const float nan = __int_as_float(0x7fc00000);
+            nA = finite_norms(nA);
+            nB = finite_norms(nB);
+            if (s0 && (bad >> g & 1u)) y0 = nan;
+            if (s1 && (bad >> g & 1u)) y1 = nan;
+            if (s2 && (bad >> (g + 8) & 1u)) y2 = nan;
+            if (s3 && (bad >> (g + 8) & 1u)) y3 = nan;
+          }
+        }
       } else {
         const float n0 = __half2float(__ushort_as_half((unsigned short)lds16(rb + v_norm_offset(D, B) + 2 * g)));
         const float n1 = __half2float(__ushort_as_half((unsigned short)lds16(rb + v_norm_offset(D, B) + 2 * (g + 8))));
@@ -290,6 +304,18 @@ __global__ void __launch_bounds__(CScored<D, B, ROT>::THREADS, CScored<D, B, ROT
   for (int i = 0; i < C::MT_W; ++i) {
     if (e0) acc[i][0] = acc[i][2] = 0.0f;
     if (e1) acc[i][1] = acc[i][3] = 0.0f;
+  }
+  // A NaN logit leaves the maximum alone: where it was the only one, the merges
+  // must not take the row for an empty one.
+  if (__any_sync(0xffffffffu, isnan(st.l0) || isnan(st.l1))) {
+    float l0 = st.l0, l1 = st.l1;
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+    if (isnan(l0)) st.m0 = fmaxf(st.m0, 0.0f);
+    if (isnan(l1)) st.m1 = fmaxf(st.m1, 0.0f);
   }
   const int64_t gid = (int64_t)(b * a.n_kv_heads + kvh) * a.n_row_groups + rg;
   const bool direct = a.n_split == 1;

@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
         if constexpr (ROT) nv[r][0] = vn[r][0], nv[r][1] = vn[r][1];
       }
       fetch_v(step_n, c_n);
-      if constexpr (ROT) {  // norms of positions that no row sees may hold any bytes
+      if constexpr (ROT) {  // norms of positions that no row sees may hold any bytes; for the rest see bad_norms
         const int pos0 = (s0 + step) * NKV;
         if (pos0 < flo || pos0 + NKV > fhi) {
           uint32_t any = 0u;
@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
           const uint32_t ma = any >> (2 * v_t), mb = any >> (2 * v_t + 8);
 #pragma unroll
           for (int r = 0; r < VR; ++r) {
-            nv[r][0] &= (ma & 1u ? 0xffffu : 0u) | (ma & 2u ? 0xffff0000u : 0u);
-            nv[r][1] &= (mb & 1u ? 0xffffu : 0u) | (mb & 2u ? 0xffff0000u : 0u);
+            nv[r][0] = finite_norms(nv[r][0]) & ((ma & 1u ? 0xffffu : 0u) | (ma & 2u ? 0xffff0000u : 0u));
+            nv[r][1] = finite_norms(nv[r][1]) & ((mb & 1u ? 0xffffu : 0u) | (mb & 2u ? 0xffff0000u : 0u));
           }
         }
       }
@@ -603,6 +603,16 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
         norms[(i & 1) * NKV + nk] = __half2float(__ushort_as_half(nrm));
         nrm = load_norm(i + 1);
       }
+      const int step0 = (s0 + i) * NKV;
+      const bool mixed = step0 < flo || step0 + NKV > fhi;  // some row does not see the whole step
+      uint32_t gn = 0u;  // ROT, mixed: not zero where a norm of key nk is not finite
+      if constexpr (ROT) {
+        if (mixed && i * NKV < nkeys) {
+#pragma unroll
+          for (int k = 0; k < C::NGRP; ++k)
+            gn |= bad_norms(*reinterpret_cast<const uint16_t*>(nbase + (int64_t)i * (4 * C::REC) + 2 * kTile * k));
+        }
+      }
       if (i > 0) {  // at once: S of the next step waits for these columns
         add_tail(i - 1, 0);
         add_tail(i - 1, 1);
@@ -623,9 +633,8 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
       // the exponential and the reciprocal, took 1598 cycles a step against 1217.)
       float z[32], mx;
       const int p0 = (s0 + i) * NKV + 32 * half;
-      const int step0 = (s0 + i) * NKV;
       uint32_t see = row.hi > 0 ? ~0u : 0u;
-      if (step0 < flo || step0 + NKV > fhi) see = static_cast<uint32_t>(scored_step_bits(row, tree, base, p0));
+      if (mixed) see = static_cast<uint32_t>(scored_step_bits(row, tree, base, p0));
       const bool masked = __any_sync(0xffffffffu, see != ~0u);
       if (form == kFormCap) {
         const uint64_t k2 = f32x2(a.mul * 2.8853900817779268f, a.mul * 2.8853900817779268f), one = f32x2(1.0f, 1.0f);
@@ -741,6 +750,14 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
         if constexpr (C::PSPLIT)
           *reinterpret_cast<uint4*>(sP + C::P_BYTES + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
+      if constexpr (ROT) {
+        uint32_t bad = mixed ? __ballot_sync(0xffffffffu, gn != 0u) & see : 0u;
+        while (bad) {  // NaN for the keys that this row sees and whose norm left V
+          const int j = __ffs(bad) - 1;
+          bad &= bad - 1u;
+          *reinterpret_cast<uint16_t*>(sP + sw128_offset(rowi, 32 * half + (j & ~7), M) + 2 * (j & 7)) = 0x7fffu;
+        }
+      }
       const float2 p2 = f32x2_get(ps);
       l_sum += p2.x + p2.y;
       fence_proxy_async();
@@ -768,9 +785,9 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
   const bool direct = a.n_split == 1;
   float* const slot = a.part + (int64_t)blockIdx.x * (M * (D + 1));
   float* const stage = reinterpret_cast<float*>(smem);
-  const float inv = l_sum > 0.0f ? 1.0f / l_sum : 0.0f;
+  const float inv = row_inv<true>(l_sum);
   if (tid < rows) {
-    const float lse = l_sum > 0.0f ? (m_used + log2f(l_sum)) * 0.6931471805599453f : -INFINITY;
+    const float lse = row_lse<true>(m_used, l_sum);
     if (direct) a.lse[((int64_t)b * a.n_q + q0 + tid / G) * a.n_q_heads + kvh * G + tid % G] = lse;
     else slot[(int64_t)M * D + tid] = lse;
   }
@@ -790,7 +807,7 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
 #pragma unroll
         for (int k = 0; k < 32; k += 4)
           *reinterpret_cast<float4*>(dst + c + k) =
-              inv > 0.0f ? make_float4(__uint_as_float(ov[k]) * inv, __uint_as_float(ov[k + 1]) * inv,
+              inv != 0.0f ? make_float4(__uint_as_float(ov[k]) * inv, __uint_as_float(ov[k + 1]) * inv,
                                        __uint_as_float(ov[k + 2]) * inv, __uint_as_float(ov[k + 3]) * inv)
                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
@@ -798,7 +815,7 @@ __global__ void __launch_bounds__(640, 1) attn_scored_tiles_kernel(ScoredArgs a)
 #pragma unroll
         for (int k = 0; k < ORH; k += 4)
           *reinterpret_cast<float4*>(dst + C::OT + 64 * (k / 32) + 32 * half + k % 32) =
-              inv > 0.0f ? make_float4(otail[k] * inv, otail[k + 1] * inv, otail[k + 2] * inv, otail[k + 3] * inv)
+              inv != 0.0f ? make_float4(otail[k] * inv, otail[k + 1] * inv, otail[k + 2] * inv, otail[k + 3] * inv)
                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
     }
@@ -904,7 +921,7 @@ __global__ void __launch_bounds__(kScoredMergeThreads) scored_merge_rows_kernel(
   for (int s = lane; s < n_split; s += 32) total += s_w[s];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+  const float inv = row_inv<true>(total);
   const float* flat = reinterpret_cast<const float*>(s_acc);
   float2 v[D / 64];
 #pragma unroll
@@ -921,7 +938,7 @@ __global__ void __launch_bounds__(kScoredMergeThreads) scored_merge_rows_kernel(
   float* const o = a.out_type == kOutF32 ? a.out + r * D
                                          : reinterpret_cast<float*>(reinterpret_cast<uint16_t*>(a.out) + r * D);
   derotate_store_row<D, ROT, true>(v, lane, a.signs, o, centroid_scale(B), a.signs2, a.out_type);
-  if (lane == 0) a.lse[r] = total > 0.0f ? m + logf(total) : -INFINITY;
+  if (lane == 0) a.lse[r] = total != 0.0f ? m + logf(total) : -INFINITY;
 }
 
 // The same for few splits (at most 32), where rows are many: one warp per row.
@@ -948,7 +965,7 @@ __global__ void __launch_bounds__(256) scored_merge_few_kernel(ScoredArgs a) {
   float total = w;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+  const float inv = row_inv<true>(total);
   float2 v[D / 64];
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) v[e] = make_float2(0.0f, 0.0f);
@@ -975,7 +992,7 @@ __global__ void __launch_bounds__(256) scored_merge_few_kernel(ScoredArgs a) {
   float* const o = a.out_type == kOutF32 ? a.out + r * D
                                          : reinterpret_cast<float*>(reinterpret_cast<uint16_t*>(a.out) + r * D);
   derotate_store_row<D, ROT, true>(v, lane, a.signs, o, centroid_scale(B), a.signs2, a.out_type);
-  if (lane == 0) a.lse[r] = total > 0.0f ? m + logf(total) : -INFINITY;
+  if (lane == 0) a.lse[r] = total != 0.0f ? m + logf(total) : -INFINITY;
 }
 
 template <int D, int B, int ROT>

@@ -1042,6 +1042,8 @@ static ckv_status run_scored(const ckv_cache* cache, const int32_t* seq_len, int
   const float kLog2e = 1.4426950408889634f, kCodes = a.tiles ? 1.0f : 16777216.0f;
   a.cap_log2 = score->softcap * kLog2e;
   a.mul = score->softcap > 0.0f ? scale * kCodes / score->softcap : scale * kCodes * kLog2e;
+  if (!std::isfinite(a.mul) || !std::isfinite(a.cap_log2))
+    return fail(CKV_ERR_INVALID_ARG, "scale, softcap or their quotient beyond float32");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = a.v_bits == 2   ? (a.rot ? ckv::launch_scored_rot2(a, st) : ckv::launch_scored_tbq2(a, st))
                         : a.v_bits == 4 ? (a.rot ? ckv::launch_scored_rot4(a, st) : ckv::launch_scored_tbq4(a, st))

@@ -169,6 +169,18 @@ __device__ __forceinline__ void store_out2(float* row, int pair, float2 v, int o
   }
 }
 
+// Weight and lse of a merged row with sum L under maximum M (log2 units): a row
+// without keys (L = 0) is 0 and -inf. ANY: a NaN sum passes through; the plain
+// decodes take it for an empty row.
+template <bool ANY>
+__device__ __forceinline__ float row_inv(float L) {
+  return (ANY ? L != 0.0f : L > 0.0f) ? 1.0f / L : 0.0f;
+}
+template <bool ANY>
+__device__ __forceinline__ float row_lse(float M, float L) {
+  return (ANY ? L != 0.0f : L > 0.0f) ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+}
+
 // Inverse rotation of one output row held by a warp (lane: dims 64 e + 2 lane
 // + c, c < 2), then the sign flip and vscale / D, stored to `orow`:
 // the unnormalised Walsh-Hadamard transform pairs the two values of a float2
@@ -371,11 +383,11 @@ __device__ __forceinline__ void decode_epilogue(SoftmaxState st, float (&acc)[MT
     float* lrow;
     row_outputs<ANY>(*direct, b, kvh, rg, r, &orow, &lrow);
     if (!orow) return;
-    const float inv = lc > 0.0f ? 1.0f / lc : 0.0f;
+    const float inv = row_inv<ANY>(lc);
 #pragma unroll
     for (int e = 0; e < E2; ++e) v[e] = make_float2(v[e].x * inv, v[e].y * inv);
     derotate_store_row<D, ROT, ANY>(v, lane, signs, orow, vscale, signs2, ANY ? direct->out_type : kOutF32);
-    if (lane == 0) *lrow = lc > 0.0f ? (mc + log2f(lc)) * 0.6931471805599453f : -INFINITY;
+    if (lane == 0) *lrow = row_lse<ANY>(mc, lc);
     return;
   }
   derotate_store_row<D, ROT>(v, lane, signs, slot + r * D, vscale, signs2);
@@ -693,7 +705,7 @@ __device__ __forceinline__ void tree_merge_tail(const DecodeArgs& a, int split, 
     const int u = tid + 256 * k;
     if (u < 2 * D) {
       const float L = s_L[u / (D / 4)];
-      const float inv = (L > 0.0f) ? 1.0f / L : 0.0f;
+      const float inv = row_inv<ANY>(L);
       reinterpret_cast<float4*>(rows)[u] =
           make_float4(acc[k].x * inv, acc[k].y * inv, acc[k].z * inv, acc[k].w * inv);
     }
@@ -707,7 +719,7 @@ __device__ __forceinline__ void tree_merge_tail(const DecodeArgs& a, int split, 
     derotate_store_row<D, 0, ANY>(v, lane, nullptr, s_out[r], kCentroidScale, nullptr, ANY ? a.out_type : kOutF32);
     if (lane == 0 && s_lse[r]) {
       const float L = s_L[r];
-      *s_lse[r] = (L > 0.0f) ? (s_M[r] + log2f(L)) * 0.6931471805599453f : -INFINITY;
+      *s_lse[r] = row_lse<ANY>(s_M[r], L);
     }
   }
 }
@@ -811,7 +823,7 @@ __device__ __forceinline__ void merge_slice(const float* slots, int n_split, int
   if (write_lse && tid < 8 && lse_rows[tid]) {
     float L = 0.0f;
     for (int ww = 0; ww < nw; ++ww) L += wsum[ww * 8 + tid];
-    *lse_rows[tid] = (L > 0.0f) ? (M + log2f(L)) * 0.6931471805599453f : -INFINITY;
+    *lse_rows[tid] = row_lse<ANY>(M, L);
   }
   // 4. Weighted sums, reduced over each unit's k lanes.
   for (int base = 0; base < nu; base += cs) {
@@ -865,7 +877,7 @@ __device__ __forceinline__ void merge_slice(const float* slots, int n_split, int
     if (sub == 0 && el < nu && out_rows[r]) {
       float L = 0.0f;
       for (int ww = 0; ww < nw; ++ww) L += wsum[ww * 8 + r];
-      const float inv = (L > 0.0f) ? 1.0f / L : 0.0f;
+      const float inv = row_inv<ANY>(L);
       if constexpr (ANY) {
         const int pair = 2 * ((u0 + el) % U);
         store_out2<true>(out_rows[r], pair, make_float2(acc.x * inv, acc.y * inv), out_type);

@@ -147,6 +147,21 @@ __device__ __forceinline__ uint64_t scored_step_bits(const RowInfo& r, bool tree
   return m;
 }
 
+// Stored norms that are not finite (V rows beyond fp16, NaN in V). In the
+// rotated tiers the norms scale V, which all rows share, and 0 times such a
+// norm would reach rows that do not see the position: where some rows see it and
+// some do not, it leaves V and the rows that see it get NaN through P'.
+// finite_norms: a pair of norms, those that are not finite as zero; bad_norms:
+// bit 0 (low) and bit 1 (high) of the pair set where it is not finite.
+__device__ __forceinline__ uint32_t bad_norms(uint32_t pair) {
+  const uint32_t t = (pair & 0x7c007c00u) + 0x04000400u;
+  return (t >> 15 & 1u) | (t >> 30 & 2u);
+}
+__device__ __forceinline__ uint32_t finite_norms(uint32_t pair) {
+  const uint32_t t = ((pair & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+  return pair & ~((t >> 15) * 0xffffu);
+}
+
 // tanh to about 4 units in the last place: x (1 - x^2/3 + 2 x^4/15 -
 // 17 x^6/315), its Taylor series, below 1/4 (the next term is 3e-7 of the
 // value there), else 1 - 2 / (1 + e^(2|x|)); the hardware's approximate tanh

@@ -613,6 +613,9 @@ typedef struct {
  * converted to fp16, exact within fp16's range). out: the same shape in
  * out_type (any ckv_dtype), 16-byte aligned; lse float32 [batch][n_q][n_q_heads].
  * n_split: 0 automatic, > 0 that many key splits.
+ * What a row does not see does not reach it, whatever it holds. A NaN logit
+ * makes the row and its lse NaN; a stored norm that is not finite makes at least
+ * its transform group's dims of the rows that see it not finite.
  * Workspace: ckv_attn_scored_workspace bytes (the same n_split), zero-filled
  * before its first use, and again before a call of other sizes (batch, heads,
  * n_q, n_split, max_seq_len, window) uses it: the header's extent goes by them.
@@ -620,7 +623,8 @@ typedef struct {
  * [0, min(capacity, max_seq_len)] or a q_len outside [0, n_q] makes every row
  * of that sequence empty and raises the device flag (2).
  * Errors: INVALID_ARG (null or misaligned pointers, types, a softcap that is
- * negative or not finite, a negative window, a scale that is not finite),
+ * negative or not finite, a negative window, a scale that is not finite or, by
+ * its factors 2^24 log2(e) or 1 / softcap, leaves float32),
  * UNSUPPORTED (head dim, head ratio, more than 65535 (sequence, kv head) pairs,
  * 524280 query rows per kv head or 2^31 - 1 query rows in all), WORKSPACE.
  */

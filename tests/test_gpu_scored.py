@@ -305,6 +305,73 @@ def test_large_caps_slopes_and_logits():
 
 # ----------------------------------------------------------------- accept --
 
+def spoil(c, at, k=None, v=None):
+    """Position `at` of every sequence packed again with one value of K or V (dim 5) replaced."""
+    x = {}
+    for name, bad in (("k", k), ("v", v)):
+        row = inputs.normal_tensor((len(c.lens), 1, c.Hkv, c.D), at, name, np.zeros(0, np.int64))
+        if bad is not None:
+            row[..., 5] = bad
+        x[name] = torch.from_numpy(row).to(DEV)
+    ckv.kv_pack(c.packed, at, x["k"], x["v"])
+    c.read()
+
+
+@pytest.mark.parametrize("n_q,Hq", [(6, 4), (5, 16), (40, 4)])
+@pytest.mark.parametrize("D,bits,rot", [(128, 3, True), (256, 2, True), (512, 4, True), (512, 3, False), (64, 3, False)])
+def test_values_that_are_not_finite_reach_only_rows_that_see_them(D, bits, rot, n_q, Hq):
+    T = 200
+    cases = [(T - 3, {}), (100, dict(doc=[[0 if i % 2 else 101 for i in range(n_q)]])), (T - 32, dict(window=30)),
+             (T - 2, dict(prefix=[T - 1], cap=20.0, alibi=True)), (T - n_q + 2, "tree")]
+    for at, kw in cases:
+        for bad in (dict(v=math.inf), dict(v=math.nan), dict(k=math.inf)):
+            c = Cache(D, 2, [T], 208, bits, rot, seed=at)
+            spoil(c, at, **bad)
+            q = queries(1, n_q, Hq, D, at)
+            if kw == "tree":
+                masks = random_tree(n_q, np.random.default_rng(n_q), width=4)[None]
+                args, see = dict(masks=masks), S.tree_rows(T, masks[0])[2]
+            else:
+                args = kw
+                see = S.causal_rows(T, n_q, kw.get("window", 0), kw.get("prefix", [0])[0], kw.get("doc", [None])[0])[2]
+            clean = ~see[:, at]
+            for n_split in (0, 1, 3):
+                out, lse, ws = run(c, [T], q, n_split=n_split, **args)
+                with np.errstate(invalid="ignore", over="ignore"):
+                    o_ref, l_ref = reference(c, [T], q, **args)
+                what = f"{D} {bits} {rot} {at} {args} {bad} {n_split}"
+                check(out[:, clean], lse[:, clean], o_ref[:, clean], l_ref[:, clean], what)
+                if "v" in bad:  # the sums do not read V
+                    seen = ~torch.isfinite(out[:, ~clean]).all(-1)
+                    assert seen.all(), what
+                    assert np.allclose(lse.cpu().numpy(), l_ref, rtol=H.LSE_RTOL, atol=H.LSE_ATOL), what
+                assert ckv.read_device_flag(ws) == 0
+
+
+@pytest.mark.parametrize("n_split", [0, 1, 5, 40])
+@pytest.mark.parametrize("D,rot,n_q", [(128, True, 5), (512, False, 1), (64, False, 30), (512, True, 40)])
+def test_nan_queries_give_nan_rows(D, rot, n_q, n_split):
+    T = 700
+    c = Cache(D, 2, [T, 0], 704, 3, rot)
+    q = queries(2, n_q, 8, D, 3)
+    want = run(c, [T, 0], q, cap=25.0, n_split=n_split)[:2]
+    q[0, n_q // 2, 3, 7] = math.nan
+    q[1, 0, 0, 0] = math.nan  # an empty row: stays empty
+    def same():
+        out, lse, ws = run(c, [T, 0], q, cap=25.0, n_split=n_split)
+        assert torch.isnan(out[0, n_q // 2, 3]).all() and torch.isnan(lse[0, n_q // 2, 3])
+        out[0, n_q // 2, 3], lse[0, n_q // 2, 3] = want[0][0, n_q // 2, 3], want[1][0, n_q // 2, 3]
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        assert ckv.read_device_flag(ws) == 0
+    same()
+    ckv.set_concurrent_kernels(True)
+    try:
+        want = run(c, [T, 0], torch.where(torch.isnan(q), torch.zeros_like(q), q), cap=25.0, n_split=n_split)[:2]
+        same()
+    finally:
+        ckv.set_concurrent_kernels(False)
+
+
 def accept(c, lens, n_q, path, count, n_of=None, stream=None):
     new, flag = ints([-7] * len(lens)), ints([0])
     ckv.tree_accept(c.packed, ints(lens), n_q, ints(path), ints(count), new, q_len=None if n_of is None else ints(n_of),

@@ -90,3 +90,9 @@ def test_accept_refusals(lib):
         (-2, dict(c=cache(D=80))), (-2, dict(c=cache(batch=65536))),
     ]:
         assert call(**kw) == status, kw
+
+
+@pytest.mark.parametrize("tree", [False, True])
+def test_scales_beyond_float32_are_refused(lib, tree):
+    for kw in (dict(scale=1e32), dict(sc=score(softcap=1e-40)), dict(sc=score(softcap=3e38))):
+        assert attend(lib, tree, **kw) == -1, kw
